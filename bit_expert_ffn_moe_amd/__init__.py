@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libbefmoe.so, the gfx950 routed-expert MoE FFN library.
+"""Thin ctypes binding of libbefmoe.so, the gfx950 routed-expert MoE FFN library
+with the operators of the decode step around the layer.
 
 Every function has the name and argument order of its C counterpart in
 include/moe.h and only marshals arguments: device buffers may be passed as
@@ -18,9 +19,12 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _SO = os.path.join(_PKG, "libbefmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_ENOTSUP, MOE_EALIGN, MOE_EWORKSPACE, MOE_ELAUNCH = 0, -1, -2, -3, -4, -5
-MOE_W_FP4_E2M1_UE8M0_K32, MOE_W_FP8_E4M3_F32_B128 = 1, 2
-MOE_DT_BF16, MOE_DT_F32 = 1, 2
+MOE_W_FP4_E2M1_UE8M0_K32, MOE_W_FP8_E4M3_F32_B128, MOE_W_INT4_BF16_GROUP = 1, 2, 3
+MOE_DT_BF16, MOE_DT_F32, MOE_DT_FP8_E4M3 = 1, 2, 3
 MOE_STATUS_BAD_EXPERT_ID, MOE_STATUS_SYNC_TIMEOUT = 1, 2
+MOE_STATUS_BAD_PAGE, MOE_STATUS_BAD_TOKEN = 4, 8
+ROPE_HALF = MOE_ROPE_HALF = 1
+ROPE_PAIRS = MOE_ROPE_PAIRS = 2
 MOE_KERNEL_GEMV_GATE_UP, MOE_KERNEL_GEMM_GATE_UP, MOE_KERNEL_GEMV_DOWN, MOE_KERNEL_GEMM_DOWN = 1, 2, 3, 4
 MOE_KERNEL_DECODE_FFN = 5
 MOE_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -61,9 +65,25 @@ class moe_expert_cache(ctypes.Structure):
                 ("bytes_copied", ctypes.c_uint64)]
 
 
+class w4_weights(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("n_out", ctypes.c_int32), ("n_in", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("zero", ctypes.c_void_p)]
+
+
+class kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("pad_", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _W = ctypes.POINTER(moe_weights)
 _C = ctypes.POINTER(moe_expert_cache)
+_L = ctypes.POINTER(w4_weights)
+_KV = ctypes.POINTER(kv_cache)
 _sigs = {
     "moe_workspace_bytes": ([_W, _i32, _i32], _sz),
     "moe_workspace_init": ([_vp, _sz, _vp], ctypes.c_int),
@@ -83,6 +103,15 @@ _sigs = {
     "moe_host_experts_scratch_bytes": ([_i32, _i32, _i32], _sz),
     "moe_forward_host_experts": ([_W, _W, _C, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _sz, _vp, _sz,
                                   _vp, _vp, _vp], ctypes.c_int),
+    "w4_linear": ([_L, _vp, _i64, _i32, _vp, _i64, _i32, _vp], ctypes.c_int),
+    "kv_append_rope": ([_KV, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _i32,
+                        _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp], ctypes.c_int),
+    "attn_workspace_bytes": ([_KV, _i32, _i32, _i32, _i32, _i32], _sz),
+    "attn_shared_prefix": ([_KV, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _i32,
+                            ctypes.c_float, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "token_logprobs_workspace_bytes": ([_i32, _i32, _i32], _sz),
+    "token_logprobs": ([_vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                        _vp], ctypes.c_int),
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "moe_device_status": ([_vp, _vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int],
                           ctypes.c_int),
@@ -235,6 +264,64 @@ def moe_forward_host_experts(host_w, slot_w, cache, w_router, x, T, k, out, out_
         ctypes.byref(host_w), ctypes.byref(slot_w), ctypes.byref(c), _ptr(w_router), _ptr(x),
         T, k, _ptr(out), out_dtype, _ptr(ws), ws_bytes, _ptr(host_scratch), host_scratch_bytes,
         _ptr(copies_done), _stream(stream), _stream(copy_stream)), "moe_forward_host_experts")
+
+
+def make_w4(fmt, n_out, n_in, group, q, scale, zero=None):
+    """Build the C descriptor of a 4-bit linear from device buffers (ints or
+    tensors).  The returned object keeps references to tensors passed in."""
+    w = w4_weights(fmt, n_out, n_in, group, _ptr(q), _ptr(scale), _ptr(zero))
+    w._keep = (q, scale, zero)
+    return w
+
+
+def w4_linear(w, x, x_stride, T, y, y_stride, y_dtype, stream=None) -> int:
+    return _check(_lib.w4_linear(ctypes.byref(w), _ptr(x), x_stride, T, _ptr(y), y_stride, y_dtype,
+                                 _stream(stream)), "w4_linear")
+
+
+def make_kv_cache(dtype, n_pages, page_size, n_kv_heads, head_dim, k, v, k_scale=None,
+                  v_scale=None):
+    """Build the C descriptor of a paged key/value cache from device buffers
+    (ints or tensors).  The returned object keeps references to tensors."""
+    c = kv_cache(dtype, n_pages, page_size, n_kv_heads, head_dim, 0, _ptr(k), _ptr(v),
+                 _ptr(k_scale), _ptr(v_scale))
+    c._keep = (k, v, k_scale, v_scale)
+    return c
+
+
+def kv_append_rope(cache, q, q_stride, n_q_heads, k, k_stride, v, v_stride, T, rope, rope_rows,
+                   rope_dim, rope_style, seq_of, pos, page_table, n_seqs, table_cols, q_out,
+                   status, stream=None) -> int:
+    return _check(_lib.kv_append_rope(
+        ctypes.byref(cache), _ptr(q), q_stride, n_q_heads, _ptr(k), k_stride, _ptr(v), v_stride, T,
+        _ptr(rope), rope_rows, rope_dim, rope_style, _ptr(seq_of), _ptr(pos), _ptr(page_table),
+        n_seqs, table_cols, _ptr(q_out), _ptr(status), _stream(stream)), "kv_append_rope")
+
+
+def attn_workspace_bytes(cache, n_seqs, q_len, n_q_heads, prefix_len, max_keys) -> int:
+    return _lib.attn_workspace_bytes(ctypes.byref(cache), n_seqs, q_len, n_q_heads, prefix_len,
+                                     max_keys)
+
+
+def attn_shared_prefix(cache, q, q_stride, n_seqs, q_len, n_q_heads, pos, prefix_pages, prefix_len,
+                       page_table, table_cols, max_keys, scale, out, lse, status, ws, ws_bytes,
+                       stream=None) -> int:
+    return _check(_lib.attn_shared_prefix(
+        ctypes.byref(cache), _ptr(q), q_stride, n_seqs, q_len, n_q_heads, _ptr(pos),
+        _ptr(prefix_pages), prefix_len, _ptr(page_table), table_cols, max_keys, scale, _ptr(out),
+        _ptr(lse), _ptr(status), _ptr(ws), ws_bytes, _stream(stream)), "attn_shared_prefix")
+
+
+def token_logprobs_workspace_bytes(T, V, n_top) -> int:
+    return _lib.token_logprobs_workspace_bytes(T, V, n_top)
+
+
+def token_logprobs(z, z_dtype, row_stride, T, V, tokens, n_top, logprob, entropy, top_ids,
+                   top_logprobs, status, ws, ws_bytes, stream=None) -> int:
+    return _check(_lib.token_logprobs(
+        _ptr(z), z_dtype, row_stride, T, V, _ptr(tokens), n_top, _ptr(logprob), _ptr(entropy),
+        _ptr(top_ids), _ptr(top_logprobs), _ptr(status), _ptr(ws), ws_bytes, _stream(stream)),
+        "token_logprobs")
 
 
 def moe_device_status(ws, stream=None, clear: bool = False) -> int:

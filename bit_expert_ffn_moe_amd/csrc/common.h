@@ -64,6 +64,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two fp32 -> two bf16 (nearest even, NaN kept), the first in the low half.
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const f2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
+}
+
 // E4M3 code of v: clamp to +-448 first (the conversion then rounds to
 // nearest even; values in (448, 464) round to 448 either way, so the clamp
 // only turns would-be overflows into the saturated code; -0 stays -0).

@@ -147,4 +147,76 @@ hipError_t launch_gemm_gate_up(const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_down(const GemmArgs& a, hipStream_t st);
 hipError_t launch_zero_words(uint32_t* p, int n, hipStream_t st);
 
+// ---- host helpers shared by the entry points (moe_api.hip) ----
+int check_device();               // MOE_OK on a gfx950, else MOE_ENOTSUP
+int launch_status(hipError_t e);  // MOE_ELAUNCH (error cleared) unless success
+
+// ---- the operators around the layer (argument checks in ops_api.hip) ----
+
+// 4-bit linear (w4.hip).
+struct W4Args {
+  const uint8_t* q;        // [N][K/2]
+  const void* scale;       // FP4: u8 [N][K/32]; INT4: bf16 [N][n_groups]
+  const uint8_t* zero;     // INT4: [N][n_groups] or null (8)
+  const uint16_t* x;
+  void* y;
+  int64_t x_stride, y_stride;
+  int T, N, K, n_groups, group_shift;
+  bool int4, y_bf16;
+};
+hipError_t launch_w4(const W4Args& a, hipStream_t st);
+
+// Paged cache append with rotation (kv.hip).
+struct KvAppendArgs {
+  void *kc, *vc;
+  float *ks, *vs;
+  const uint16_t *q, *k, *v;
+  uint16_t* q_out;
+  int64_t q_stride, k_stride, v_stride;
+  const float* rope;
+  const int32_t *seq_of, *pos, *table;
+  uint32_t* status;
+  int T, Hq, Hkv, D, R, rope_rows, n_seqs, table_cols, n_pages, page_shift;
+  int iters;               // set by the launcher: head groups per block
+  bool fp8, pairs;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st);
+
+// Token log probabilities (logprobs.hip): W waves of kLogprobChunk elements a row.
+constexpr int kLogprobChunk = 2048;
+struct LogprobArgs {
+  const void* z;
+  int64_t row_stride;
+  int T, V, W, n_top;
+  const int32_t* tokens;
+  float *logprob, *entropy, *top_logprobs;
+  int32_t* top_ids;
+  uint32_t* status;
+  float *pm, *pl, *ps;          // [T][W] partials
+  unsigned long long* pk;       // [T][n_top][W] candidate keys
+};
+hipError_t launch_logprobs(const LogprobArgs& a, bool bf16, hipStream_t st);
+
+// Shared-prefix attention (attn.hip).
+struct AttnArgs {
+  const void *k, *v;
+  const float *ks, *vs;
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t *pos, *prefix_pages, *table;
+  uint16_t* out;
+  float* lse;
+  uint32_t* status;
+  float* po;                    // [part][n_tok][Hq][D] unnormalised sums
+  float2* pml;                  // [part][n_tok][Hq] maximum (log2 units), weight
+  float scale_log2;             // scale * log2(e)
+  int B, Q, n_tok, Hq, Hkv, G, D;
+  int table_cols, n_pages, page_shift, prefix_len, max_keys;
+  bool fp8;
+  // split: 16 x rt rows per item, chunks (keys) and parts of the two kinds
+  int prefix_rt, prefix_blocks, prefix_chunk, n_prefix_parts;
+  int own_rt, own_blocks, own_chunk, n_own_parts;
+};
+hipError_t launch_attn(const AttnArgs& a, hipStream_t st);
+
 }  // namespace bef

@@ -135,6 +135,8 @@ Layout layout_w(const moe_weights* w, int T, int k) {
 // One-time check per device that it is a gfx950 (the only global state).
 std::atomic<int> g_arch_ok[64];
 
+}  // namespace
+
 int check_device() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
@@ -163,6 +165,8 @@ int launch_status(hipError_t e) {
   }
   return MOE_OK;
 }
+
+namespace {
 
 // T = 0 is an empty batch: valid, and the entry points return MOE_OK after
 // checking their other arguments, reading, writing and launching nothing.

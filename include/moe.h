@@ -1,5 +1,7 @@
 /*
- * moe.h -- C ABI of the MI355X (gfx950) routed-expert MoE FFN library.
+ * moe.h -- C ABI of the MI355X (gfx950) routed-expert MoE FFN library, and
+ * of the operators that surround the layer in a decode step (4-bit linears,
+ * a paged key/value cache, attention over it, token log probabilities).
  *
  * The layer: 256 routed experts, top-6 per token, plus one always-on shared
  * expert (tcti.cn post on DeepSeek-V4-Flash on 4x RTX 2080 Ti, section
@@ -64,11 +66,14 @@ enum {
 enum {
   MOE_W_FP4_E2M1_UE8M0_K32 = 1, /* E2M1 codes 2/byte (element 2j in bits 0-3),
                                    one UE8M0 byte per 32 inputs               */
-  MOE_W_FP8_E4M3_F32_B128 = 2   /* E4M3 codes, one fp32 per 128x128 block     */
+  MOE_W_FP8_E4M3_F32_B128 = 2,  /* E4M3 codes, one fp32 per 128x128 block     */
+  MOE_W_INT4_BF16_GROUP = 3     /* (w4_linear only) unsigned 4-bit codes, 2/byte
+                                   as above, one bf16 scale and an optional u8
+                                   zero point per group of inputs             */
 };
 
-/* Activation / output dtypes. */
-enum { MOE_DT_BF16 = 1, MOE_DT_F32 = 2 };
+/* Activation / output dtypes (MOE_DT_FP8_E4M3: key/value caches only). */
+enum { MOE_DT_BF16 = 1, MOE_DT_F32 = 2, MOE_DT_FP8_E4M3 = 3 };
 
 /* Device status word bits (see moe_device_status).  MOE_STATUS_SYNC_TIMEOUT:
  * on the small-T router or the one-token path, a block waiting for the
@@ -76,6 +81,10 @@ enum { MOE_DT_BF16 = 1, MOE_DT_F32 = 2 };
  * call are invalid, and the workspace must go through moe_workspace_init
  * again before its next use (a late value could outlive the clean-up). */
 enum { MOE_STATUS_BAD_EXPERT_ID = 1u, MOE_STATUS_SYNC_TIMEOUT = 2u };
+
+/* Bits that the decode-step operators OR into the caller's `status` word (a
+ * device uint32_t, 4-byte aligned, cleared by the caller; NULL: not reported). */
+enum { MOE_STATUS_BAD_PAGE = 4u, MOE_STATUS_BAD_TOKEN = 8u };
 
 /* Stacked expert weights, expert-major; slot E (the last) is the shared
  * expert, which must have the same intermediate size as the routed ones.
@@ -301,6 +310,142 @@ int moe_forward_host_experts(const moe_weights* host_w, const moe_weights* slot_
                              int32_t T, int32_t k, void* out, int32_t out_dtype, void* ws,
                              size_t ws_bytes, void* host_scratch, size_t host_scratch_bytes,
                              void* copies_done, void* stream, void* copy_stream);
+
+/* ---- Operators of the decode step around the layer --------------------------
+ * The conventions at the top hold: device pointers, host-checked arguments,
+ * nothing allocated or synchronised, the work enqueued on `stream`, calls
+ * capturable in a HIP graph.  Workspaces need no initialisation.  Where a limit
+ * is not stated otherwise, 0 <= T <= 262144 tokens, T = 0 an empty batch.
+ * Strides are in elements.  Index arrays (tokens, positions, pages) need 4-byte
+ * alignment, everything else 16 bytes. */
+
+/* 4-bit weights of a linear, [n_out][n_in] row-major, two codes per byte
+ * (element 2j in bits 0-3), n_in a multiple of 32.
+ *   MOE_W_FP4_E2M1_UE8M0_K32: group 32, scale u8 [n_out][n_in/32] UE8M0 (255 is
+ *     NaN), zero NULL; w = e2m1(code) * 2^(scale - 127)
+ *   MOE_W_INT4_BF16_GROUP: group 32, 64 or 128, G = ceil(n_in / group), scale
+ *     bf16 [n_out][G], zero u8 [n_out][G] or NULL (8 everywhere);
+ *     w = scale * (code - zero)
+ * The descriptor is host memory, read during the call only. */
+typedef struct w4_weights {
+  int32_t format;
+  int32_t n_out;
+  int32_t n_in;
+  int32_t group;
+  const void* q;
+  const void* scale;
+  const void* zero;
+} w4_weights;
+
+/* y[t][n] = sum_k x[t][k] w[n][k]: the projections around the expert layer for
+ * a few tokens (any T is valid; tuned up to 64).  Codes and activations
+ * enter the products unrounded, sums are fp32, y is rounded once.
+ *   x [T][n_in] bf16, rows x_stride apart (a multiple of 8, >= n_in)
+ *   y [T][n_out] bf16 or f32 (y_dtype), rows y_stride >= n_out apart
+ * n_out and n_in up to 2^20 (MOE_ENOTSUP beyond). */
+int w4_linear(const w4_weights* w, const uint16_t* x, int64_t x_stride, int32_t T, void* y,
+              int64_t y_stride, int32_t y_dtype, void* stream);
+
+/* A paged key/value cache.  k and v are [n_pages][n_kv_heads][page_size]
+ * [head_dim], bf16 or E4M3; an E4M3 cache has one fp32 scale per row in k_scale
+ * and v_scale, [n_pages][n_kv_heads][page_size] (NULL for bf16).  page_size is
+ * a power of two, 16 to 1024; head_dim 64, 128 or 256; n_kv_heads <= 1024.
+ * The descriptor is host memory, read during the call only. */
+typedef struct kv_cache {
+  int32_t dtype;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t pad_;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} kv_cache;
+
+/* How pairs are laid out in a rotated head of rope_dim elements: element i
+ * with i + rope_dim/2, or 2i with 2i + 1. */
+enum { MOE_ROPE_HALF = 1, MOE_ROPE_PAIRS = 2 };
+
+/* Rotates q and k by their tokens' positions and appends k and v to the cache.
+ * Token t is key number pos[t] of sequence seq_of[t]: its slot is
+ * pos % page_size of page page_table[seq][pos / page_size].  A pair (a, b) of
+ * the first rope_dim elements of a head becomes (a c - b s, b c + a s) in fp32,
+ * each operation rounded, with c = rope[pos][i], s = rope[pos][rope_dim/2 + i];
+ * the other elements and v are taken as they are.  Cache rows are bf16 (nearest
+ * even), or E4M3 by the rule of act_quant_fp8 over the whole head row.
+ *   q [T][n_q_heads][head_dim] bf16, token rows q_stride apart; n_q_heads = 0
+ *     (q, q_out NULL): keys and values only
+ *   k, v [T][n_kv_heads][head_dim] bf16, token rows k_stride, v_stride apart
+ *     (multiples of 8; a fused projection's output can be passed in place)
+ *   rope [rope_rows][rope_dim] f32: cosines, then sines; rope_dim a multiple of
+ *     16 up to head_dim, or 0 (no rotation, rope NULL)
+ *   seq_of, pos [T] int32; page_table [n_seqs][table_cols] int32
+ *   q_out [T][n_q_heads][head_dim] bf16, contiguous; must not overlap an input
+ * A negative seq_of or pos is padding: nothing is written for the token.  So is
+ * a token whose sequence, position or page is out of range, which also sets
+ * MOE_STATUS_BAD_PAGE.  Two tokens of one call for the same slot race. */
+int kv_append_rope(const kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,
+                   const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                   int32_t T, const float* rope, int32_t rope_rows, int32_t rope_dim,
+                   int32_t rope_style, const int32_t* seq_of, const int32_t* pos,
+                   const int32_t* page_table, int32_t n_seqs, int32_t table_cols, uint16_t* q_out,
+                   uint32_t* status, void* stream);
+
+/* Workspace bytes of attn_shared_prefix with these arguments (0 if they are
+ * invalid). */
+size_t attn_workspace_bytes(const kv_cache* cache, int32_t n_seqs, int32_t q_len,
+                            int32_t n_q_heads, int32_t prefix_len, int32_t max_keys);
+
+/* Attention over the cache for a batch whose sequences share their first
+ * prefix_len keys, which are read once for the whole batch.  Query token
+ * t = b * q_len + i of sequence b sees the keys 0 .. pos[t] of its sequence:
+ * those below prefix_len in the pages prefix_pages [ceil(prefix_len /
+ * page_size)], the others in page_table[b] (indexed from key 0, as kv_append_rope
+ * does; its entries below prefix_len / page_size are not read).  prefix_len
+ * may end inside a page, and may be 0.
+ *   q [n_seqs * q_len][n_q_heads][head_dim] bf16, token rows q_stride apart (a
+ *     multiple of 8); n_q_heads a multiple of n_kv_heads, head h reading kv head
+ *     h / (n_q_heads / n_kv_heads)
+ *   pos [n_seqs * q_len] int32; negative: the token sees no key (padding)
+ *   max_keys: an upper bound of pos + 1 (prefix_len <= max_keys <=
+ *     table_cols * page_size); keys from max_keys on are not seen and a token
+ *     that would see one sets MOE_STATUS_BAD_PAGE
+ *   scale: positive; o = sum_j softmax_j(scale q.k_j) v_j
+ *   out [n_seqs * q_len][n_q_heads][head_dim] bf16
+ *   lse [n_seqs * q_len][n_q_heads] f32 or NULL: log sum_j exp(scale q.k_j)
+ * A row that sees no key gives out 0 and lse -inf.  What the cache holds at keys
+ * that a row does not see (NaN included) does not enter it.  A page number
+ * outside the cache hides its keys and sets MOE_STATUS_BAD_PAGE.  Scores and sums
+ * are fp32; probabilities are rounded to bf16 for the product with V.
+ * n_seqs * q_len <= 262144, n_q_heads <= 1024, and n_seqs * q_len * n_q_heads
+ * <= 2^24. */
+int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t n_seqs,
+                       int32_t q_len, int32_t n_q_heads, const int32_t* pos,
+                       const int32_t* prefix_pages, int32_t prefix_len, const int32_t* page_table,
+                       int32_t table_cols, int32_t max_keys, float scale, uint16_t* out,
+                       float* lse, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of token_logprobs (0 on invalid arguments). */
+size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top);
+
+/* Log probabilities under softmax(z[t]) of the given tokens, the entropy of the
+ * distribution, and the n_top best alternatives by (z descending, id ascending,
+ * NaN last).
+ *   z [T][V] bf16 or f32, rows row_stride >= V apart (any alignment of the rows)
+ *   tokens [T] int32 and logprob [T] f32, or both NULL; an id outside [0, V) is
+ *     no token: logprob 0 (an id >= V also sets MOE_STATUS_BAD_TOKEN)
+ *   entropy [T] f32 (nats) or NULL
+ *   top_ids [T][n_top] int32, top_logprobs [T][n_top] f32, 0 <= n_top <=
+ *     min(64, V) (both may be NULL when n_top = 0)
+ * A logit of -inf has probability 0.  A row of nothing else gives log
+ * probabilities of -inf and entropy 0; a row with +inf or NaN gives NaN.
+ * 1 <= V <= 2^24. */
+int token_logprobs(const void* z, int32_t z_dtype, int64_t row_stride, int32_t T, int32_t V,
+                   const int32_t* tokens, int32_t n_top, float* logprob, float* entropy,
+                   int32_t* top_ids, float* top_logprobs, uint32_t* status, void* ws,
+                   size_t ws_bytes, void* stream);
 
 /* A static string naming a status code. */
 const char* moe_status_string(int status);
