@@ -140,11 +140,16 @@ def _ptr(a):
     return a.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream around it
+# (0.2 us instead of 3.8 us a call); torch versions without it take the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(s):
     if s is None:
-        import sys
-        torch = sys.modules.get("torch")
-        if torch is not None and torch.cuda.is_available():
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
+        if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(s, int):
