@@ -19,9 +19,12 @@
 // columns) of each of its 8 keys, coalesced, and packs them with byte
 // permutes -- no LDS and no transposed copy of the cache.
 //
-// Scores, statistics and sums are fp32.  P is rounded to bf16 (2^-9 relative
-// per key, the price of the matrix cores with bf16 V); the weights summed are
-// the unrounded ones.
+// Scores, statistics and sums are fp32.  P is rounded for the matrix cores: to
+// bf16 beside bf16 V (the key at a row's maximum has P = 1, exactly), to fp16
+// beside E4M3 V, where P carries the row's scale and no value of it is exact;
+// the weights summed are the unrounded ones.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -66,13 +69,47 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&d)[W]) 
 }
 
 __device__ __forceinline__ float quad_max(float v) {  // over the 4 lane groups
-  v = fmaxf(v, xchg16(v));
-  return fmaxf(v, xchg32(v));
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t w = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float quad_sum(float v) {
   v += xchg16(v);
   return v + xchg32(v);
 }
+
+// two fp32 -> two fp16, nearest even
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const h2_t v = {(_Float16)lo, (_Float16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// V^T P^T: bf16, or fp16 for an FP8 cache (E4M3 values are fp16 values, and P
+// then keeps 11 bits)
+typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+template <bool F16>
+__device__ __forceinline__ v4f_t mfma_pv(const uint4 a, const uint4 b, v4f_t c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a),
+                                                  __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
+  else
+    return mfma(a, b, c);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint4 pack_p(const float (&w)[8]) {
+  if constexpr (F16)
+    return make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
+                      pack_f16(w[6], w[7]));
+  else
+    return make_uint4(f32x2_to_bf16x2(w[0], w[1]), f32x2_to_bf16x2(w[2], w[3]),
+                      f32x2_to_bf16x2(w[4], w[5]), f32x2_to_bf16x2(w[6], w[7]));
+}
+
+// page lists are read through the scalar cache (nothing writes them here)
+typedef __attribute__((address_space(4))) const int32_t const_i32;
 
 // keys the item reads: [lo, hi) of one page list
 struct Range {
@@ -82,193 +119,274 @@ struct Range {
 
 }  // namespace
 
-// Query rows per item and the limits of a row.
+// The keys a token sees.
 __device__ __forceinline__ int row_limit(const AttnArgs& a, int t) {
   const int p = a.pos[t];
   return p < 0 ? 0 : min(p + 1, a.max_keys);
 }
 
-// One block (4 waves): RT x 16 rows from row r0 of `rows` (row r is token
-// t0 + r / G, query head h G + r % G) over the keys [lo, hi); 32-key tiles are
-// dealt out over the waves and joined in LDS at the end.
-template <int D, bool FP8, int RT>
+// Raises the power of two `vref` to bound the lanes' scales vm (2^-100 at
+// least); `rescale` takes the sums over to it.
+template <class F>
+__device__ __forceinline__ void raise_vref(float vm, float& vref, F&& rescale) {
+  vm = __uint_as_float(__float_as_uint(quad_max(vm)) & 0x7f800000u);
+  vm = fmaxf(vm + vm, 0x1p-100f);
+  if (__ballot(vm > vref)) {
+    rescale(vref / vm);
+    vref = vm;
+  }
+}
+
+__device__ __forceinline__ float max8(const float (&x)[8]) {
+  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+               fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+}
+
+// The running maximum m of a lane column (log2 units), given this tile's largest
+// scores: P = 2^(score - m).  m is raised where a score passes it by more than
+// 3, so P is at most 8 and the sums are rescaled a few times, not at every
+// tile that holds a new maximum (most of the first dozens); a key that stands
+// out by more than that has P = 1 exactly.
+template <class F>
+__device__ __forceinline__ void raise_max(float mx, float& m, F&& rescale) {
+  if (__ballot(mx > m + 3.0f)) {
+    const float mn = quad_max(fmaxf(mx, m));
+    rescale(mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn));
+    m = mn;
+  }
+}
+
+// Whether key j of the range [lo, hi) lies in a page outside the cache.
+__device__ __forceinline__ bool bad_key(const AttnArgs& a, const int32_t* pages, int j, int lo,
+                                        int hi) {
+  const int pg = pages[max(lo, min(j, hi - 1)) >> a.page_shift];
+  return pg < 0 || pg >= a.n_pages;
+}
+// One block (4 waves) over the keys of rg for up to 64 rows, r0.. of `rows` (row
+// r is token t0 + r / G, query head h G + r % G).  The waves are 4 / wk row
+// sets of 16 rows by wk key sets: 32-key tiles are dealt out over the key sets,
+// whose sums are joined in LDS at the end.
+//
+// A tile's K is dead once the scores are formed and its V once they are
+// multiplied, so the next tile's are loaded into the same registers right
+// then: a load has the rest of a tile's work to arrive in.
+template <int D, bool FP8>
 __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int r0, int rows,
-                                          const Range& rg, int part, float* lds) {
+                                          const Range& rg, int part, int wk, float* lds) {
   constexpr int NS = D / 32;        // 32-column steps of the score product
   constexpr int VD = D / 16;        // columns per lane of V and O
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  constexpr int ES = FP8 ? 1 : 2;
+  constexpr int NK = FP8 ? NS / 2 : NS;      // 16-byte K loads per 16 keys
+  constexpr int VW = VD * ES / 4;            // dwords per key of this lane's V columns
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int page_size = 1 << a.page_shift;
+  const int kset = wv % wk, rset = wv / wk;
+  const int slots = (1 << a.page_shift) - 1;
+  r0 += rset * 16;
 
-  // this lane's query of each row tile, its operand and its limit
-  uint4 q[RT][NS];
-  int lim[RT], tok[RT], head[RT];
-  int maxlim = 0, minlim = 0x7fffffff;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = r0 + 16 * rt + c;
-    const int rr = min(r, rows - 1);
-    tok[rt] = t0 + rr / a.G;
-    head[rt] = h * a.G + rr % a.G;
-    lim[rt] = r < rows ? row_limit(a, tok[rt]) : 0;
-    if (lim[rt] > 0) {
-      maxlim = max(maxlim, lim[rt]);
-      minlim = min(minlim, lim[rt]);
-    }
-    // column order of the score product: bf16 K, step s of group g holds
-    // columns 32 s + 8 g; FP8 K, steps 2u and 2u+1 the halves of the 16 codes
-    // from 64 u + 16 g
-    const uint16_t* qr = a.q + (size_t)tok[rt] * a.q_stride + (size_t)head[rt] * D;
+  // this lane's query, its operand and its limit.  Column order of the score
+  // product: bf16 K, step s of group g holds columns 32 s + 8 g; FP8 K, steps 2u
+  // and 2u+1 the halves of the 16 codes from 64 u + 16 g
+  const bool in = r0 + c < rows;
+  const int rr = min(r0 + c, rows - 1);
+  const int tok = t0 + rr / a.G, head = h * a.G + rr % a.G;
+  const int lim = in ? row_limit(a, tok) : 0;
+  const int maxlim = __builtin_amdgcn_readfirstlane(wave_max_all(lim));
+  const int minlim = __builtin_amdgcn_readfirstlane(wave_min_all(lim > 0 ? lim : 0x7fffffff));
+  uint4 q[NS];
+  {
+    const uint16_t* qr = a.q + (size_t)tok * a.q_stride + (size_t)head * D;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
-      q[rt][s] = *reinterpret_cast<const uint4*>(
+      q[s] = *reinterpret_cast<const uint4*>(
           qr + (FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g));
   }
-  maxlim = wave_max_all(maxlim);
-  minlim = wave_min_all(minlim);
-  const int hi = min(rg.hi, maxlim);
+  const int lo = rg.lo, hi = min(rg.hi, maxlim);
 
-  v4f_t o[RT][VD];
-  float m[RT], l[RT];
+  v4f_t o[VD];
+  float m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    m[rt] = -INFINITY, l[rt] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VD; ++j) o[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int j = 0; j < VD; ++j) o[j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  float vref = 0.0f;  // FP8: o is in units of this power of two
 
-  const int first = (rg.lo & ~31) + 32 * wv;
-  for (int j0 = first; j0 < hi; j0 += 128) {
-    // the pages of the two 16-key halves (the second may lie past the last key)
-    const uint8_t *kb[2], *vb[2];
-    const float *ksb[2], *vsb[2];
+  // the 16-key halves' first cache rows (the second half may lie past the last
+  // key: any row of a valid page serves), through the scalar cache
+  struct Rows {
+    size_t row[2];
     bool bad[2];
+  };
+  const const_i32* pages = (const const_i32*)rg.pages;
+  auto rows_at = [&](int j0) {
+    Rows r;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int ju = max(rg.lo, min(j0 + 16 * u, hi - 1));
-      int pg = __builtin_amdgcn_readfirstlane(rg.pages[ju >> a.page_shift]);
-      bad[u] = pg < 0 || pg >= a.n_pages;
-      pg = bad[u] ? 0 : pg;
-      const int slot = (j0 + 16 * u) & (page_size - 1);
-      const size_t row = ((size_t)pg * a.Hkv + h) * page_size + slot;
-      kb[u] = (const uint8_t*)a.k + row * D * (FP8 ? 1 : 2);
-      vb[u] = (const uint8_t*)a.v + row * D * (FP8 ? 1 : 2);
-      ksb[u] = a.ks + row, vsb[u] = a.vs + row;
+      const int ju = max(lo, min(j0 + 16 * u, hi - 1));
+      const int pg = pages[ju >> a.page_shift];
+      r.bad[u] = pg < 0 || pg >= a.n_pages;
+      r.row[u] = (((size_t)(r.bad[u] ? 0 : pg) * a.Hkv + h) << a.page_shift) +
+                 ((j0 + 16 * u) & slots);
     }
-    if ((bad[0] || bad[1]) && lane == 0 && a.status) set_status(a.status, MOE_STATUS_BAD_PAGE);
-
-    // K operand and V rows
-    uint4 kf[2][NS];
+    return r;
+  };
+  const uint32_t ko = (c * D + (FP8 ? 16 : 8) * g) * ES, vo = (4 * g * D + VD * c) * ES;
+  uint4 kr[2][NK];
+  float4 ks4[2], vs4[2];
+  uint32_t vr[8][VW];
+  auto load_k = [&](const Rows& r) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* kb = (const uint8_t*)a.k + r.row[u] * (D * ES);
+#pragma unroll
+      for (int s = 0; s < NK; ++s) kr[u][s] = *reinterpret_cast<const uint4*>(kb + ko + 64 * s);
       if constexpr (FP8) {
-#pragma unroll
-        for (int s = 0; s < NS; s += 2) {
-          const uint4 x = *reinterpret_cast<const uint4*>(kb[u] + c * D + 32 * s + 16 * g);
-          kf[u][s] = fp8x8(x.x, x.y);
-          kf[u][s + 1] = fp8x8(x.z, x.w);
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-          kf[u][s] = *reinterpret_cast<const uint4*>(kb[u] + (c * D + 32 * s + 8 * g) * 2);
+        ks4[u] = *reinterpret_cast<const float4*>(a.ks + r.row[u] + 4 * g);
+        vs4[u] = *reinterpret_cast<const float4*>(a.vs + r.row[u] + 4 * g);
       }
-    constexpr int VW = FP8 ? VD / 4 : VD / 2;  // dwords per key of this lane's V columns
-    uint32_t vr[8][VW];
+    }
+  };
+  auto load_v = [&](const Rows& r) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      load_dwords((const uint8_t*)a.v + r.row[e >> 2] * (D * ES) + vo + (e & 3) * (D * ES), vr[e]);
+  };
+
+  // V rows that no row of the item sees may hold anything: cleared.  A
+  // non-finite V that only some rows see must not meet the others' P = 0 (0 x inf
+  // is NaN): true where the tile has one.
+  auto leaks = [&](int j0, const Rows& cur) -> bool {
+    bool leak = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      load_dwords(vb[e >> 2] + ((4 * g + (e & 3)) * D + VD * c) * (FP8 ? 1 : 2), vr[e]);
-    }
-    float kscale[8], vscale[8];
-    if constexpr (FP8) {
+      const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
+      const bool keep = j >= lo && j < hi && !cur.bad[e >> 2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float4 x = *reinterpret_cast<const float4*>(ksb[u] + 4 * g);
-        const float4 y = *reinterpret_cast<const float4*>(vsb[u] + 4 * g);
-        kscale[4 * u] = x.x, kscale[4 * u + 1] = x.y, kscale[4 * u + 2] = x.z, kscale[4 * u + 3] = x.w;
-        vscale[4 * u] = y.x, vscale[4 * u + 1] = y.y, vscale[4 * u + 2] = y.z, vscale[4 * u + 3] = y.w;
+      for (int i = 0; i < VW; ++i) {
+        vr[e][i] = keep ? vr[e][i] : 0u;
+        if (FP8)
+          leak |= (((vr[e][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+        else
+          leak |= (vr[e][i] & 0x7f80u) == 0x7f80u || (vr[e][i] & 0x7f800000u) == 0x7f800000u;
+      }
+      if constexpr (FP8) {
+        const float4 v = vs4[e >> 2];
+        const float x = (e & 3) == 0 ? v.x : (e & 3) == 1 ? v.y : (e & 3) == 2 ? v.z : v.w;
+        leak |= keep && !(fabsf(x) < INFINITY);
       }
     }
-    // a tile that is not wholly inside every row's keys is masked; V rows no
-    // row of the item sees are cleared, as they may hold anything
-    const bool edge = j0 < rg.lo || j0 + 32 > min(hi, minlim) || bad[0] || bad[1];
-    bool leak = false;  // a non-finite V that some row of the item must not see
-    if (edge) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
-        const bool keep = j >= rg.lo && j < hi && !bad[e >> 2];
-#pragma unroll
-        for (int i = 0; i < VW; ++i) {
-          vr[e][i] = keep ? vr[e][i] : 0u;
-          if (FP8) {
-            const uint32_t x = vr[e][i] & 0x7f7f7f7fu;
-            leak |= ((x + 0x01010101u) & 0x80808080u) != 0;
-          } else {
-            leak |= (vr[e][i] & 0x7f80u) == 0x7f80u || (vr[e][i] & 0x7f800000u) == 0x7f800000u;
-          }
-        }
-        if (FP8) {
-          vscale[e] = keep ? vscale[e] : 0.0f;
-          leak |= !(fabsf(vscale[e]) < INFINITY);
-        }
-      }
-      leak = __ballot(leak) != 0;
+    return __ballot(leak) != 0;
+  };
+
+  // One tile, its K and V loaded (or on their way): SLOW, one limit at a time.
+  // `after_k` and `after_v` run when K and V are dead.  False: nothing was done,
+  // the tile needs SLOW.
+  auto tile = [&](auto slow, int j0, const Rows& cur, auto&& after_k, auto&& after_v) -> bool {
+    constexpr bool SLOW = decltype(slow)::value;
+    const bool bad = cur.bad[0] || cur.bad[1];
+    if (bad && lane == 0 && a.status) set_status(a.status, MOE_STATUS_BAD_PAGE);
+    // a tile that is not wholly inside every row's keys is masked
+    const bool edge = SLOW || j0 < lo || j0 + 32 > min(hi, minlim) || bad;
+    auto key_of = [&](int e) { return j0 + 16 * (e >> 2) + 4 * g + (e & 3); };
+    auto inside = [&](int e) { return key_of(e) >= lo && key_of(e) < hi && !cur.bad[e >> 2]; };
+
+    if (!SLOW && edge && leaks(j0, cur)) {
+      after_k();
+      after_v();
+      return false;
     }
 
-    // scores and probabilities
-    uint4 p[RT];
+    // scores
+    float x[8];
+    {
+      uint4 kf[2][NS];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          if constexpr (FP8) {
+            const uint4 k = kr[u][s / 2];
+            kf[u][s] = (s & 1) ? fp8x8(k.z, k.w) : fp8x8(k.x, k.y);
+          } else {
+            kf[u][s] = kr[u][s];
+          }
+        }
       v4f_t s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        s0 = mfma(kf[0][s], q[rt][s], s0);
-        s1 = mfma(kf[1][s], q[rt][s], s1);
+        s0 = mfma(kf[0][s], q[s], s0);
+        s1 = mfma(kf[1][s], q[s], s1);
       }
-      float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] *= FP8 ? a.scale_log2 * kscale[e] : a.scale_log2;
-        if (edge) {
-          const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          if (j < rg.lo || j >= lim[rt] || j >= hi || bad[e >> 2]) x[e] = -INFINITY;
+      for (int e = 0; e < 4; ++e) x[e] = s0[e], x[4 + e] = s1[e];
+    }
+    float vscale[8];
+    if constexpr (FP8) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float kk[4] = {ks4[u].x, ks4[u].y, ks4[u].z, ks4[u].w};
+        const float vv[4] = {vs4[u].x, vs4[u].y, vs4[u].z, vs4[u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[4 * u + e] *= kk[e];
+          vscale[4 * u + e] = vv[e];
         }
       }
-      float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                       fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      mx = quad_max(fmaxf(mx, m[rt]));
-      if (__ballot(mx > m[rt])) {
-        const float f = m[rt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[rt] - mx);
-        l[rt] *= f;
-#pragma unroll
-        for (int j = 0; j < VD; ++j) o[rt][j] *= f;
-        m[rt] = mx;
-      }
-      const float mu = m[rt] == -INFINITY ? 0.0f : m[rt];
-      float w[8];
+    }
+    after_k();
+
+    if constexpr (FP8) {
+      // P v_scale enters the product in fp16: o in units of a power of two that
+      // bounds the scales, so that it stays at most 1
+      float vm = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        w[e] = __builtin_amdgcn_exp2f(x[e] - mu);
-        l[rt] += w[e];
-        if (FP8) w[e] = edge && x[e] == -INFINITY ? 0.0f : w[e] * vscale[e];
+        if (edge) {
+          if (!inside(e)) vscale[e] = 0.0f;
+          vm = fmaxf(vm, fabsf(vscale[e]) < INFINITY ? fabsf(vscale[e]) : 0.0f);
+        } else {
+          vm = fmaxf(vm, fabsf(vscale[e]));
+        }
       }
-      p[rt] = make_uint4(f32x2_to_bf16x2(w[0], w[1]), f32x2_to_bf16x2(w[2], w[3]),
-                         f32x2_to_bf16x2(w[4], w[5]), f32x2_to_bf16x2(w[6], w[7]));
+      raise_vref(vm, vref, [&](float f) {
+#pragma unroll
+        for (int j = 0; j < VD; ++j) o[j] *= f;
+      });
+      const float inv = 1.0f / vref;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) vscale[e] *= inv;
     }
+
+    // probabilities
+    if (edge) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!inside(e) || key_of(e) >= lim) x[e] = -INFINITY;
+    }
+    raise_max(max8(x) * a.scale_log2, m, [&](float f) {
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < VD; ++j) o[j] *= f;
+    });
+    const float mu = m == -INFINITY ? 0.0f : m;
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale_log2, -mu));
+      l += w[e];
+      if (FP8) w[e] = edge && x[e] == -INFINITY ? 0.0f : w[e] * vscale[e];
+    }
+    const uint4 p = pack_p<FP8>(w);
 
     // O^T += V^T P^T, column set j of the lanes
     auto v_operand = [&](int j) -> uint4 {
       uint32_t d[4];
       if constexpr (FP8) {
-        // byte j%4 of keys 0..3 and 4..7
+        // byte j%4 of two keys, then both converted
         const uint32_t sel = 0x0c0c0400u + 0x0101u * (j & 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t two =
-              __builtin_amdgcn_perm(vr[2 * i + 1][j / 4], vr[2 * i][j / 4], sel);
-          d[i] = fp8_lo(two);
-        }
+        for (int i = 0; i < 4; ++i)
+          d[i] = __builtin_bit_cast(
+              uint32_t,
+              e4m3x2_lo(__builtin_amdgcn_perm(vr[2 * i + 1][j / 4], vr[2 * i][j / 4], sel)));
       } else {
         const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
 #pragma unroll
@@ -277,111 +395,112 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
       }
       return make_uint4(d[0], d[1], d[2], d[3]);
     };
-    if (!leak) {
+    if constexpr (!SLOW) {
 #pragma unroll
-      for (int j = 0; j < VD; ++j) {
-        const uint4 vf = v_operand(j);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma(vf, p[rt], o[rt][j]);
-      }
+      for (int j = 0; j < VD; ++j) o[j] = mfma_pv<FP8>(v_operand(j), p, o[j]);
     } else {
-      // 0 x inf is NaN: rows with different limits one limit at a time, the
-      // values past it cleared
-      int done = -1;
-      while (true) {
-        int next = 0x7fffffff;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          if (lim[rt] > done) next = min(next, lim[rt]);
-        next = wave_min_all(next);
+      for (int done = -1;;) {
+        const int next = wave_min_all(lim > done ? lim : 0x7fffffff);
         if (next == 0x7fffffff) break;
         done = next;
-        uint32_t keep[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          keep[e] = j0 + 16 * (e >> 2) + 4 * g + (e & 3) < done ? 0xffffffffu : 0u;
 #pragma unroll
         for (int j = 0; j < VD; ++j) {
-          uint4 vf = v_operand(j);
-          vf.x &= (keep[0] & 0xffffu) | (keep[1] & 0xffff0000u);
-          vf.y &= (keep[2] & 0xffffu) | (keep[3] & 0xffff0000u);
-          vf.z &= (keep[4] & 0xffffu) | (keep[5] & 0xffff0000u);
-          vf.w &= (keep[6] & 0xffffu) | (keep[7] & 0xffff0000u);
+          const uint4 v = v_operand(j);
+          uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const v4f_t n = mfma(vf, p[rt], o[rt][j]);
-            if (lim[rt] == done) o[rt][j] = n;
-          }
+          for (int i = 0; i < 4; ++i)
+            d[i] &= (key_of(2 * i) < done ? 0xffffu : 0u) |
+                    (key_of(2 * i + 1) < done ? 0xffff0000u : 0u);
+          const v4f_t n = mfma_pv<FP8>(make_uint4(d[0], d[1], d[2], d[3]), p, o[j]);
+          if (lim == done) o[j] = n;
         }
       }
     }
+    after_v();
+    return true;
+  };
+
+  const int step = 32 * wk, first = (lo & ~31) + 32 * kset;
+  bool leaked = false;
+  {
+    Rows cur{}, nxt{};
+    if (first < hi) {
+      cur = rows_at(first);
+      load_k(cur);
+      load_v(cur);
+    }
+    for (int j0 = first; j0 < hi; j0 += step) {
+      const bool more = j0 + step < hi;
+      if (more) nxt = rows_at(j0 + step);
+      leaked |= !tile(std::false_type{}, j0, cur, [&] { if (more) load_k(nxt); },
+                      [&] { if (more) load_v(nxt); });
+      cur = nxt;
+    }
+  }
+  // tiles set aside: found again among the ones at an edge
+  if (leaked) {
+    for (int j0 = first; j0 < hi; j0 += step) {
+      const Rows cur = rows_at(j0);
+      if (!(j0 < lo || j0 + 32 > min(hi, minlim) || cur.bad[0] || cur.bad[1])) continue;
+      load_k(cur);
+      load_v(cur);
+      if (leaks(j0, cur)) tile(std::true_type{}, j0, cur, [] {}, [] {});
+    }
   }
 
-  // the four waves' sums joined: two rounds through LDS
-  float* lml = lds;                        // [4][RT][64][2]: m, l (l summed over the groups)
-  float* lo = lds + 4 * RT * 64 * 2;       // [2][RT * VD * 4][64]
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    l[rt] = quad_sum(l[rt]);
-    lml[((wv * RT + rt) * 64 + lane) * 2] = m[rt];
-    lml[((wv * RT + rt) * 64 + lane) * 2 + 1] = l[rt];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, lml[((w * RT + rt) * 64 + lane) * 2]);
-    float L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float mw = lml[((w * RT + rt) * 64 + lane) * 2];
-      if (mw != -INFINITY)
-        L += lml[((w * RT + rt) * 64 + lane) * 2 + 1] * __builtin_amdgcn_exp2f(mw - M);
+  // the key sets' sums joined through LDS, in halves
+  l = quad_sum(l);
+  float2* lml = reinterpret_cast<float2*>(lds);  // [wave][64]: m, l
+  float* lo_ = lds + 4 * 64 * 2;                 // [2][VD * 4][64]
+  float f = FP8 ? vref : 1.0f;
+  if (wk > 1) {
+    lml[wv * 64 + lane] = make_float2(m, l);
+    __syncthreads();
+    float M = -INFINITY, L = 0.0f;
+    for (int w = rset * wk; w < (rset + 1) * wk; ++w) M = fmaxf(M, lml[w * 64 + lane].x);
+    for (int w = rset * wk; w < (rset + 1) * wk; ++w) {
+      const float2 ml = lml[w * 64 + lane];
+      if (ml.x != -INFINITY) L += ml.y * __builtin_amdgcn_exp2f(ml.x - M);
     }
-    const float f = m[rt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[rt] - M);
-#pragma unroll
-    for (int j = 0; j < VD; ++j) o[rt][j] *= f;
-    m[rt] = M, l[rt] = L;
+    f = m == -INFINITY ? 0.0f : f * __builtin_amdgcn_exp2f(m - M);
+    m = M, l = L;
   }
 #pragma unroll
-  for (int half = 2; half > 0; half >>= 1) {
-    if (wv >= half && wv < 2 * half) {
+  for (int j = 0; j < VD; ++j) o[j] *= f;
+  for (int half = wk >> 1; half > 0; half >>= 1) {
+    float* mine = lo_ + (rset * half + kset % half) * (VD * 4 * 64) + lane;
+    if (kset >= half && kset < 2 * half) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int j = 0; j < VD; ++j)
 #pragma unroll
-        for (int j = 0; j < VD; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            lo[(((wv - half) * RT * VD + rt * VD + j) * 4 + r) * 64 + lane] = o[rt][j][r];
+        for (int r = 0; r < 4; ++r) mine[(j * 4 + r) * 64] = o[j][r];
     }
     __syncthreads();
-    if (wv < half) {
+    if (kset < half) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int j = 0; j < VD; ++j)
 #pragma unroll
-        for (int j = 0; j < VD; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            o[rt][j][r] += lo[((wv * RT * VD + rt * VD + j) * 4 + r) * 64 + lane];
+        for (int r = 0; r < 4; ++r) o[j][r] += mine[(j * 4 + r) * 64];
     }
     __syncthreads();
   }
-  if (wv) return;
+  if (kset || !in) return;
+  const size_t row = ((size_t)part * a.n_tok + tok) * a.Hq + head;
+  if (g == 0) a.pml[row] = make_float2(lim ? m : -INFINITY, lim ? l : 0.0f);
+  float* dst = a.po + row * D + VD * 4 * g;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if (r0 + 16 * rt + c >= rows) continue;
-    const size_t row = ((size_t)part * a.n_tok + tok[rt]) * a.Hq + head[rt];
-    const bool none = lim[rt] == 0;
-    if (g == 0) a.pml[row] = make_float2(none ? -INFINITY : m[rt], none ? 0.0f : l[rt]);
-    float* dst = a.po + row * D + VD * 4 * g;
+  for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int j = 0; j < VD; j += 4)
-        *reinterpret_cast<float4*>(dst + VD * r + j) =
-            make_float4(o[rt][j][r], o[rt][j + 1][r], o[rt][j + 2][r], o[rt][j + 3][r]);
-  }
+    for (int j = 0; j < VD; j += 4)
+      *reinterpret_cast<float4*>(dst + VD * r + j) =
+          make_float4(o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]);
+}
+
+// The keys that the longest-sighted of sequence b's tokens sees (wave-uniform).
+__device__ __forceinline__ int seq_limit(const AttnArgs& a, int b) {
+  int lim = 0;
+  for (int i = threadIdx.x & 63; i < a.Q; i += 64) lim = max(lim, row_limit(a, b * a.Q + i));
+  return __builtin_amdgcn_readfirstlane(wave_max_all(lim));
 }
 
 // Number of a sequence's own parts in use: its longest row's keys past the
@@ -391,101 +510,521 @@ __device__ __forceinline__ int own_parts(const AttnArgs& a, int lim) {
   return lim > a.prefix_len ? (lim - lo + a.own_chunk - 1) / a.own_chunk : 0;
 }
 
-// Prefix items first (they are the long ones), then the sequences' own.
-template <int D, bool FP8, int RTP, int RTS>
-__global__ __launch_bounds__(256) void attn_part_kernel(AttnArgs a) {
-  constexpr int RT = RTP > RTS ? RTP : RTS;
-  __shared__ float lds[4 * RT * 64 * 2 + 2 * RT * (D / 16) * 4 * 64];
-  int item = blockIdx.x;
-  const int rows_p = a.n_tok * a.G, rows_s = a.Q * a.G;
-  const int np = a.n_prefix_parts * a.Hkv * a.prefix_blocks;
+// An item of the grid: a range of keys for one kv head and a block of rows.
+struct Item {
+  Range rg;
+  int h, t0, rows, rb, part, wk;
+};
+
+// The first `np` items are the prefix's, the others the sequences' own; false
+// if the sequence ends before the part.
+__device__ __forceinline__ bool item_of(const AttnArgs& a, int item, int np, Item& it) {
   if (item < np) {
-    const int rb = item % a.prefix_blocks;
-    item /= a.prefix_blocks;
-    const int h = item % a.Hkv, part = item / a.Hkv;
-    const Range rg = {a.prefix_pages, part * a.prefix_chunk,
-                      min((part + 1) * a.prefix_chunk, a.prefix_len)};
-    attn_item<D, FP8, RTP>(a, h, 0, rb * 16 * RTP, rows_p, rg, part, lds);
-  } else {
-    item -= np;
-    const int rb = item % a.own_blocks;
-    item /= a.own_blocks;
-    const int h = item % a.Hkv;
-    item /= a.Hkv;
-    const int b = item % a.B, part = item / a.B;
-    int lim = 0;
-    for (int i = 0; i < a.Q; ++i) lim = max(lim, row_limit(a, b * a.Q + i));
-    if (part >= own_parts(a, lim)) return;
-    const int base = (a.prefix_len & ~31) + part * a.own_chunk;
-    const Range rg = {a.table + (size_t)b * a.table_cols, max(base, a.prefix_len),
-                      min(base + a.own_chunk, a.max_keys)};
-    attn_item<D, FP8, RTS>(a, h, b * a.Q, rb * 16 * RTS, rows_s, rg, a.n_prefix_parts + part, lds);
+    // a prefix part's row blocks on one XCD (block ids alike modulo 8), whose L2
+    // then holds the keys they share
+    const int pairs = np / a.prefix_blocks;
+    int pair, rb;
+    if (pairs % 8 == 0) {
+      const int q = item >> 3;
+      rb = q % a.prefix_blocks;
+      pair = (q / a.prefix_blocks) * 8 + (item & 7);
+    } else {
+      rb = item % a.prefix_blocks;
+      pair = item / a.prefix_blocks;
+    }
+    it.rb = rb, it.h = pair % a.Hkv, it.part = pair / a.Hkv;
+    it.t0 = 0, it.rows = a.n_tok * a.G, it.wk = a.prefix_wk;
+    it.rg = {a.prefix_pages, it.part * a.prefix_chunk,
+             min((it.part + 1) * a.prefix_chunk, a.prefix_len)};
+    return true;
+  }
+  item -= np;
+  it.rb = item % a.own_blocks;
+  item /= a.own_blocks;
+  it.h = item % a.Hkv;
+  item /= a.Hkv;
+  const int b = item % a.B, part = item / a.B;
+  if (part >= own_parts(a, seq_limit(a, b))) return false;
+  const int base = (a.prefix_len & ~31) + part * a.own_chunk;
+  it.t0 = b * a.Q, it.rows = a.Q * a.G, it.wk = a.own_wk, it.part = a.n_prefix_parts + part;
+  it.rg = {a.table + (size_t)b * a.table_cols, max(base, a.prefix_len),
+           min(base + a.own_chunk, a.max_keys)};
+  return true;
+}
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(256, D < 256 ? 3 : 2) void attn_part_kernel(AttnArgs a, int np) {
+  __shared__ __align__(8) float lds[4 * 64 * 2 + 2 * (D / 16) * 4 * 64];
+  Item it;
+  if (!item_of(a, blockIdx.x, np, it)) return;
+  attn_item<D, FP8>(a, it.h, it.t0, it.rb * 16 * (4 / it.wk), it.rows, it.rg, it.part, it.wk, lds);
+}
+
+// ---- many rows: keys staged in LDS for eight waves of rows -------------------
+// A block takes 8 x RT x 16 rows; tiles of 64 keys go through LDS, loaded into
+// registers while the tile before multiplies.  K lands as rows of bf16, V
+// transposed (a row per column, the eight key slots of a lane group together:
+// one 16-byte read is an operand), each with its 16-byte chunks permuted by row
+// so that reads of 16 rows meet distinct banks.  An FP8 cache is converted
+// here, once for all the waves.
+template <int D, bool FP8, int RT>
+__global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
+  constexpr int NS = D / 32, VD = D / 16, ES = FP8 ? 1 : 2;
+  constexpr int KC = D * ES / 16;                 // 16-byte pieces of a K row
+  constexpr int NKL = 64 * KC / 512 ? 64 * KC / 512 : 1;   // K pieces per thread
+  constexpr int CH = D / 8;                       // 16-byte chunks of an LDS K row
+  __shared__ uint4 lk[2][64][CH];
+  __shared__ uint4 lv[2][D][8];                   // [column][8 chunks of 8 key slots]
+  __shared__ float lks[2][64], lvs[2][64];
+  // marks by buffer: the tile (its first key) that holds a non-finite V, a bad page;
+  // whether a wave has set a group aside
+  __shared__ int lleak[2], lbad[2], lslow;
+  Item itm;
+  if (!item_of(a, blockIdx.x, np, itm)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int h = itm.h, rows = itm.rows;
+  const int rblk = itm.rb * 128 * RT, r0 = rblk + wv * 16 * RT;
+
+  uint4 q[RT][NS];
+  int lim[RT];
+  int minlim = 0x7fffffff, maxlim = 0;
+  auto row_of = [&](int rt, int& tok, int& head) {
+    const int rr = min(r0 + 16 * rt + c, rows - 1);
+    tok = itm.t0 + rr / a.G;
+    head = h * a.G + rr % a.G;
+    return r0 + 16 * rt + c < rows;
+  };
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    int tok, head;
+    const bool in = row_of(rt, tok, head);
+    lim[rt] = in ? row_limit(a, tok) : 0;
+    if (lim[rt] > 0) minlim = min(minlim, lim[rt]);
+    const uint16_t* qr = a.q + (size_t)tok * a.q_stride + (size_t)head * D;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) q[rt][s] = *reinterpret_cast<const uint4*>(qr + 32 * s + 8 * g);
+  }
+  minlim = __builtin_amdgcn_readfirstlane(wave_min_all(minlim));
+  // keys any row of the block sees (every wave walks the same tiles)
+  for (int r = rblk + lane; r < min(rows, rblk + 128 * RT); r += 64)
+    maxlim = max(maxlim, row_limit(a, itm.t0 + r / a.G));
+  maxlim = __builtin_amdgcn_readfirstlane(wave_max_all(maxlim));
+  const int lo = itm.rg.lo, hi = min(itm.rg.hi, maxlim);
+
+  v4f_t o[RT][VD];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY, l[rt] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VD; ++j) o[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  }
+  float vref = 0.0f;
+
+  // this thread's pieces of a tile: K piece i is 16 bytes of key kkey + i x
+  // (keys per round); V unit i is columns 8 vcol.. of keys 2 vkp, 2 vkp + 1
+  constexpr int KPR = 512 / KC;     // keys per round of K loads
+  const int kkey = tid / KC, kpc = tid % KC;
+  constexpr int VU = D / 8 < 64 ? D / 8 : 64;
+  const int vcol = tid % VU, vkp0 = tid / VU;    // 512 / VU key pairs per round
+  constexpr int VPR = 512 / VU;
+  constexpr int NV = 32 / VPR ? 32 / VPR : 1;
+  static_assert(NV * VPR >= 32, "V rounds");
+  uint4 kreg[NKL];
+  uint32_t vreg[NV][2][FP8 ? 2 : 4];
+  float sreg = 0.0f;
+  const int32_t* pages = itm.rg.pages;
+  // the pages of this thread's pieces, fetched a tile ahead of them (a V unit's
+  // two keys share one)
+  int pgk[NKL], pgv[NV], pgs = 0;
+  auto page_of = [&](int j) { return pages[max(lo, min(j, hi - 1)) >> a.page_shift]; };
+  auto load_pages = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < NKL; ++i) pgk[i] = page_of(j0 + kkey + KPR * i);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) pgv[i] = page_of(j0 + 2 * (vkp0 + VPR * i));
+    if (FP8) pgs = page_of(j0 + (tid & 63));
+  };
+  bool badp = false;
+  // cache row of key j in page pg (any valid row where j is outside [lo, hi))
+  auto row_at = [&](int j, int pg, bool& ok) {
+    const bool bad = pg < 0 || pg >= a.n_pages;
+    if (bad && a.status) set_status(a.status, MOE_STATUS_BAD_PAGE);
+    badp |= bad;
+    ok = j >= lo && j < hi && !bad;
+    return (((size_t)(bad ? 0 : pg) * a.Hkv + h) << a.page_shift) +
+           (j & ((1 << a.page_shift) - 1));
+  };
+  uint32_t okbits = 0;  // of the loaded tile: K piece / V key / scale in range
+  auto load_tile = [&](int j0) {
+    okbits = 0;
+    badp = false;
+#pragma unroll
+    for (int i = 0; i < NKL; ++i)
+      if (64 * KC >= 512 || tid < 64 * KC) {
+        bool ok;
+        const size_t row = row_at(j0 + kkey + KPR * i, pgk[i], ok);
+        kreg[i] = *reinterpret_cast<const uint4*>((const uint8_t*)a.k + row * (D * ES) + 16 * kpc);
+      }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (VPR <= 32 || vkp0 < 32) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          bool ok;
+          const size_t row = row_at(j0 + 2 * (vkp0 + VPR * i) + k, pgv[i], ok);
+          load_dwords((const uint8_t*)a.v + row * (D * ES) + 8 * ES * vcol, vreg[i][k]);
+          okbits |= ok ? 1u << (2 * i + k) : 0u;
+        }
+      }
+    if (FP8 && tid < 128) {
+      bool ok;
+      const size_t row = row_at(j0 + (tid & 63), pgs, ok);
+      sreg = (tid < 64 ? a.ks : a.vs)[row];
+      okbits |= ok ? 0x80000000u : 0u;
+    }
+  };
+  auto swz_k = [](int r, int ch) { return ch ^ (CH >= 16 ? r & 15 : (r >> 1) & 7); };
+  auto swz_v = [](int d, int ch) { return ch ^ (((d >> 1) ^ (d >> 4)) & 7); };
+  auto store_tile = [&](int buf, int j0) {
+#pragma unroll
+    for (int i = 0; i < NKL; ++i)
+      if (64 * KC >= 512 || tid < 64 * KC) {
+        const int r = kkey + KPR * i;
+        const uint4 x = kreg[i];
+        if constexpr (FP8) {
+          lk[buf][r][swz_k(r, 2 * kpc)] = fp8x8(x.x, x.y);
+          lk[buf][r][swz_k(r, 2 * kpc + 1)] = fp8x8(x.z, x.w);
+        } else {
+          lk[buf][r][swz_k(r, kpc)] = x;
+        }
+      }
+    bool leak = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (VPR <= 32 || vkp0 < 32) {
+        const int kp = vkp0 + VPR * i;
+        // rows outside the item's keys may hold anything: cleared
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (!(okbits >> (2 * i + k) & 1u))
+#pragma unroll
+            for (int w = 0; w < (FP8 ? 2 : 4); ++w) vreg[i][k][w] = 0u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int w = 0; w < (FP8 ? 2 : 4); ++w) {
+            const uint32_t x = vreg[i][k][w];
+            if (FP8)
+              leak |= (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+            else
+              leak |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+          }
+        // key slot of key 2 kp: {4g.., 16 + 4g..} of each 32 together
+        const int k32 = (2 * kp) & 31;
+        const int slot = ((2 * kp) & 32) + 8 * ((k32 & 15) >> 2) + (k32 & 3) + (k32 & 16 ? 4 : 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t two;
+          if constexpr (FP8)
+            two = __builtin_bit_cast(
+                uint32_t, e4m3x2_lo(__builtin_amdgcn_perm(vreg[i][1][e / 4], vreg[i][0][e / 4],
+                                                          0x0c0c0400u + 0x0101u * (e & 3))));
+          else
+            two = __builtin_amdgcn_perm(vreg[i][1][e / 2], vreg[i][0][e / 2],
+                                        (e & 1) ? 0x07060302u : 0x05040100u);
+          const int d = 8 * vcol + e;
+          reinterpret_cast<uint32_t*>(&lv[buf][d][swz_v(d, slot >> 3)])[(slot & 7) >> 1] = two;
+        }
+      }
+    if (FP8 && tid < 128) {
+      const bool ok = okbits >> 31;
+      if (tid < 64) {
+        lks[buf][tid] = sreg;
+      } else {
+        lvs[buf][tid & 63] = ok ? sreg : 0.0f;
+        leak |= ok && !(fabsf(sreg) < INFINITY);
+      }
+    }
+    if (leak) lleak[buf] = j0;
+    if (badp) lbad[buf] = j0;
+  };
+
+  // The tiles in turn.  SLOW: only the groups set aside by the first walk (false:
+  // sets them aside, and says so): keys that only some of the wave's rows see, one of
+  // them with a non-finite V, which must not meet the other rows' P = 0 (0 x inf is
+  // NaN).
+  auto walk = [&](auto slow) -> bool {
+    constexpr bool SLOW = decltype(slow)::value;
+    bool aside = false;
+    int buf = 0, j0 = lo & ~31;
+    if (j0 < hi) {
+      load_pages(j0);
+      load_tile(j0);
+      load_pages(j0 + 64);
+    }
+    for (; j0 < hi; j0 += 64, buf ^= 1) {
+    store_tile(buf, j0);
+    __syncthreads();
+    if (j0 + 64 < hi) {
+      load_tile(j0 + 64);
+      load_pages(j0 + 128);
+    }
+    const bool any_leak = lleak[buf] == j0, any_bad = lbad[buf] == j0;
+    // Where registers allow, the scores of both halves first: their products run
+    // under the first half's softmax (128 columns and two row tiles: one half at a time,
+    // 131 us instead of 147 for 512 rows of a kv head over 32768 keys)
+    constexpr int BOTH = RT == 1 || D == 64 ? 2 : 1;
+#pragma unroll 1
+    for (int kh = 0; kh < 2; kh += BOTH) {
+    float x[BOTH][RT][8];
+#pragma unroll
+    for (int kb = 0; kb < BOTH; ++kb) {
+      const int kt = kh + kb;
+      v4f_t s0[RT], s1[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s0[rt] = s1[rt] = v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int ra = 32 * kt + c, rb = ra + 16;
+        const uint4 k0 = lk[buf][ra][swz_k(ra, 4 * s + g)], k1 = lk[buf][rb][swz_k(rb, 4 * s + g)];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          s0[rt] = mfma(k0, q[rt][s], s0[rt]);
+          s1[rt] = mfma(k1, q[rt][s], s1[rt]);
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[kb][rt][e] = s0[rt][e], x[kb][rt][4 + e] = s1[rt][e];
+    }
+#pragma unroll
+    for (int kb = 0; kb < BOTH; ++kb) {
+      const int kt = kh + kb;
+      const int jk = j0 + 32 * kt;
+      auto key_of = [&](int e) { return jk + 16 * (e >> 2) + 4 * g + (e & 3); };
+      const bool edge = jk < lo || jk + 32 > min(hi, minlim) || any_bad;
+      if (SLOW != (edge && any_leak)) {
+        aside = true;
+        continue;
+      }
+      float vscale[8];
+      if constexpr (FP8) {
+        float vm = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float4 kk = *reinterpret_cast<const float4*>(&lks[buf][32 * kt + 16 * u + 4 * g]);
+          const float4 vv = *reinterpret_cast<const float4*>(&lvs[buf][32 * kt + 16 * u + 4 * g]);
+          const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, v4[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) x[kb][rt][4 * u + e] *= k4[e];
+            vscale[4 * u + e] = v4[e];
+            vm = fmaxf(vm, fabsf(v4[e]) < INFINITY ? fabsf(v4[e]) : 0.0f);
+          }
+        }
+        raise_vref(vm, vref, [&](float f) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int j = 0; j < VD; ++j) o[rt][j] *= f;
+        });
+        const float inv = 1.0f / vref;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vscale[e] *= inv;
+      }
+      uint4 p[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (edge) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (key_of(e) < lo || key_of(e) >= min(hi, lim[rt]) ||
+                (any_bad && bad_key(a, pages, key_of(e), lo, hi)))
+              x[kb][rt][e] = -INFINITY;
+        }
+        raise_max(max8(x[kb][rt]) * a.scale_log2, m[rt], [&](float f) {
+          l[rt] *= f;
+#pragma unroll
+          for (int j = 0; j < VD; ++j) o[rt][j] *= f;
+        });
+        const float mu = m[rt] == -INFINITY ? 0.0f : m[rt];
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[e] = __builtin_amdgcn_exp2f(fmaf(x[kb][rt][e], a.scale_log2, -mu));
+          l[rt] += w[e];
+          if (FP8) w[e] = edge && x[kb][rt][e] == -INFINITY ? 0.0f : w[e] * vscale[e];
+        }
+        p[rt] = pack_p<FP8>(w);
+      }
+      auto v_operand = [&](int j) {
+        const int d = 16 * j + c;
+        return lv[buf][d][swz_v(d, 4 * kt + g)];
+      };
+      if constexpr (!SLOW) {
+#pragma unroll
+        for (int j = 0; j < VD; ++j) {
+          const uint4 vf = v_operand(j);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
+        }
+      } else {
+        // one limit at a time, the values past it cleared
+        int done = -1;
+        while (true) {
+          int next = 0x7fffffff;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            if (lim[rt] > done) next = min(next, lim[rt]);
+          next = wave_min_all(next);
+          if (next == 0x7fffffff) break;
+          done = next;
+          uint32_t keep[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) keep[e] = key_of(e) < done ? 0xffffffffu : 0u;
+#pragma unroll
+          for (int j = 0; j < VD; ++j) {
+            uint4 vf = v_operand(j);
+            vf.x &= (keep[0] & 0xffffu) | (keep[1] & 0xffff0000u);
+            vf.y &= (keep[2] & 0xffffu) | (keep[3] & 0xffff0000u);
+            vf.z &= (keep[4] & 0xffffu) | (keep[5] & 0xffff0000u);
+            vf.w &= (keep[6] & 0xffffu) | (keep[7] & 0xffff0000u);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              const v4f_t n = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
+              if (lim[rt] == done) o[rt][j] = n;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+    }
+    }
+    }
+    return aside;
+  };
+  if (tid < 2) lleak[tid] = lbad[tid] = -1;
+  if (tid == 2) lslow = 0;
+  __syncthreads();
+  if (walk(std::false_type{})) lslow = 1;
+  __syncthreads();
+  if (lslow) walk(std::true_type{});
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    int tok, head;
+    const float lsum = quad_sum(l[rt]);
+    if (!row_of(rt, tok, head)) continue;
+    const size_t row = ((size_t)itm.part * a.n_tok + tok) * a.Hq + head;
+    const bool none = lim[rt] == 0;
+    if (g == 0) a.pml[row] = make_float2(none ? -INFINITY : m[rt], none ? 0.0f : lsum);
+    float* dst = a.po + row * D + 4 * g;
+    const float f = FP8 ? vref : 1.0f;
+#pragma unroll
+    for (int j = 0; j < VD; ++j)
+      *reinterpret_cast<float4*>(dst + 16 * j) =
+          make_float4(o[rt][j][0] * f, o[rt][j][1] * f, o[rt][j][2] * f, o[rt][j][3] * f);
   }
 }
 
-// One lane group of D/4 lanes per output row: the row's parts weighted by
-// 2^(m - M) and normalised.
+// Joins a row's parts, weighted by 2^(m - M), and normalises.  D/4 lanes hold a
+// row's columns; 4 such groups a row take its parts in turn, 8 loads at a time.
+constexpr int kJoinGroups = 4;
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  constexpr int LPR = D / 4;
-  const int64_t row = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  if (row >= (int64_t)a.n_tok * a.Hq) return;
-  const int t = (int)(row / a.Hq), d = 4 * (threadIdx.x % LPR);
-  const int b = t / a.Q;
-  int lim = 0;
-  for (int i = 0; i < a.Q; ++i) lim = max(lim, row_limit(a, b * a.Q + i));
-  const int parts = a.n_prefix_parts + own_parts(a, lim);
-  const size_t stride = (size_t)a.n_tok * a.Hq;
-  float M = -INFINITY;
-  for (int p = 0; p < parts; ++p) M = fmaxf(M, a.pml[p * stride + row].x);
-  float L = 0.0f;
+  constexpr int LPR = D / 4, RPB = 256 / (LPR * kJoinGroups), U = 8;
+  __shared__ float4 so[RPB][kJoinGroups][LPR];
+  __shared__ float2 sml[RPB][kJoinGroups];
+  const int ln = threadIdx.x % LPR, pg = threadIdx.x / LPR % kJoinGroups,
+            rl = threadIdx.x / (LPR * kJoinGroups);
+  const int64_t nrows = (int64_t)a.n_tok * a.Hq;
+  const int64_t row_ = (int64_t)blockIdx.x * RPB + rl;
+  const int64_t row = row_ < nrows ? row_ : nrows - 1;
+  const int t = (int)(row / a.Hq), b = t / a.Q;
+  const int parts = a.n_prefix_parts + own_parts(a, seq_limit(a, b));  // (a wave has one row)
+  float M = -INFINITY, L = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = a.pml[p * stride + row];
-    if (ml.x == -INFINITY) continue;
-    const float f = __builtin_amdgcn_exp2f(ml.x - M);
-    const float4 v = *reinterpret_cast<const float4*>(a.po + (p * stride + row) * D + d);
-    L = fmaf(f, ml.y, L);
+  for (int p0 = pg; p0 < parts; p0 += kJoinGroups * U) {
+    float2 ml[U];
+    float4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const size_t at = (size_t)min(p0 + kJoinGroups * i, parts - 1) * nrows + row;
+      ml[i] = a.pml[at];
+      v[i] = *reinterpret_cast<const float4*>(a.po + at * D + 4 * ln);
+    }
+    float mn = M;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (p0 + kJoinGroups * i >= parts) ml[i].x = -INFINITY;
+      mn = fmaxf(mn, ml[i].x);
+    }
+    if (mn == -INFINITY) continue;
+    const float f0 = __builtin_amdgcn_exp2f(M - mn);
+    M = mn;
+    L *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (ml[i].x != -INFINITY) {  // (a part without keys may hold anything)
+        const float f = __builtin_amdgcn_exp2f(ml[i].x - M);
+        L = fmaf(f, ml[i].y, L);
+        o.x = fmaf(f, v[i].x, o.x), o.y = fmaf(f, v[i].y, o.y);
+        o.z = fmaf(f, v[i].z, o.z), o.w = fmaf(f, v[i].w, o.w);
+      }
+  }
+  so[rl][pg][ln] = o;
+  if (ln == 0) sml[rl][pg] = make_float2(M, L);
+  __syncthreads();
+  if (pg || row_ >= nrows) return;
+  for (int k = 0; k < kJoinGroups; ++k) M = fmaxf(M, sml[rl][k].x);
+  L = 0.0f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < kJoinGroups; ++k) {
+    if (sml[rl][k].x == -INFINITY) continue;
+    const float f = __builtin_amdgcn_exp2f(sml[rl][k].x - M);
+    const float4 v = so[rl][k][ln];
+    L = fmaf(f, sml[rl][k].y, L);
     o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
     o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
   }
   const bool none = M == -INFINITY;
   if (!none) o.x /= L, o.y /= L, o.z /= L, o.w /= L;
-  *reinterpret_cast<uint2*>(a.out + row * D + d) =
+  *reinterpret_cast<uint2*>(a.out + row * D + 4 * ln) =
       make_uint2(f32x2_to_bf16x2(o.x, o.y), f32x2_to_bf16x2(o.z, o.w));
-  if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-  if (a.status && d == 0 && a.pos[t] >= a.max_keys) set_status(a.status, MOE_STATUS_BAD_PAGE);
+  if (a.lse && ln == 0) a.lse[row] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  if (a.status && ln == 0 && a.pos[t] >= a.max_keys) set_status(a.status, MOE_STATUS_BAD_PAGE);
 }
 
 namespace {
 
-template <int D, bool FP8, int RTP>
-void launch_rows(const AttnArgs& a, int grid, hipStream_t st) {
-  if (a.own_rt == 1)
-    attn_part_kernel<D, FP8, RTP, 1><<<grid, 256, 0, st>>>(a);
+// Both sorts of item in one launch where they are of one kind (AttnArgs).
+template <int D, bool FP8, int KIND>
+void launch_parts(const AttnArgs& a, hipStream_t st) {
+  const int np = a.prefix_kind == KIND ? a.n_prefix_parts * a.Hkv * a.prefix_blocks : 0;
+  const int no = a.own_kind == KIND ? a.n_own_parts * a.B * a.Hkv * a.own_blocks : 0;
+  if (np + no == 0) return;
+  if constexpr (KIND == 0)
+    attn_part_kernel<D, FP8><<<np + no, 256, 0, st>>>(a, np);
   else
-    attn_part_kernel<D, FP8, RTP, 2><<<grid, 256, 0, st>>>(a);
+    attn_tile_kernel<D, FP8, KIND><<<np + no, 512, 0, st>>>(a, np);
 }
 
 template <int D, bool FP8>
-void launch_dim(const AttnArgs& a, int grid, hipStream_t st) {
-  if (a.prefix_rt == 1)
-    launch_rows<D, FP8, 1>(a, grid, st);
-  else
-    launch_rows<D, FP8, 2>(a, grid, st);
+void launch_dim(const AttnArgs& a, hipStream_t st) {
+  launch_parts<D, FP8, 1>(a, st);
+  if constexpr (D < 256) launch_parts<D, FP8, 2>(a, st);
+  launch_parts<D, FP8, 0>(a, st);
 }
 
 template <int D>
 void launch_all(const AttnArgs& a, hipStream_t st) {
-  const int grid = a.n_prefix_parts * a.Hkv * a.prefix_blocks +
-                   a.n_own_parts * a.B * a.Hkv * a.own_blocks;
-  if (grid > 0) {
-    if (a.fp8)
-      launch_dim<D, true>(a, grid, st);
-    else
-      launch_dim<D, false>(a, grid, st);
-  }
-  constexpr int RPB = 256 / (D / 4);
+  if (a.fp8)
+    launch_dim<D, true>(a, st);
+  else
+    launch_dim<D, false>(a, st);
+  constexpr int RPB = 256 / (D / 4 * kJoinGroups);
   const int64_t rows = (int64_t)a.n_tok * a.Hq;
   attn_join_kernel<D><<<(unsigned)((rows + RPB - 1) / RPB), 256, 0, st>>>(a);
 }

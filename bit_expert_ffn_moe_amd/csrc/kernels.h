@@ -213,9 +213,12 @@ struct AttnArgs {
   int B, Q, n_tok, Hq, Hkv, G, D;
   int table_cols, n_pages, page_shift, prefix_len, max_keys;
   bool fp8;
-  // split: 16 x rt rows per item, chunks (keys) and parts of the two kinds
-  int prefix_rt, prefix_blocks, prefix_chunk, n_prefix_parts;
-  int own_rt, own_blocks, own_chunk, n_own_parts;
+  // split of the prefix's items and of the sequences' own: kind (0: 16 rows a
+  // wave, keys straight to registers; 1, 2: 16 x kind rows, keys through LDS),
+  // wk (kind 0: key sets that a block's 4 waves form, the rest are row sets),
+  // row blocks, keys per part, parts
+  int prefix_kind, prefix_wk, prefix_blocks, prefix_chunk, n_prefix_parts;
+  int own_kind, own_wk, own_blocks, own_chunk, n_own_parts;
 };
 hipError_t launch_attn(const AttnArgs& a, hipStream_t st);
 

@@ -9,6 +9,12 @@
 #include "moe.h"
 
 using namespace bef;
+#ifndef WANTP
+#define WANTP 256
+#define MINP 256
+#define WANTO 1024
+#define MINO 256
+#endif
 
 namespace {
 
@@ -49,16 +55,26 @@ int check_rows(int64_t stride, int64_t n) {
 // ---- attention: how the work is split ---------------------------------------
 namespace {
 
-constexpr int kAttnBlocks = 1024;  // about four per CU: the chip is filled once
-constexpr int kAttnMinChunk = 256;
+// How `rows` query rows of a kv head are taken (see AttnArgs).
+void split_rows(int rows, int D, int* kind, int* wk, int* blocks) {
+  if (rows <= 64) {
+    *kind = 0;
+    *wk = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;
+    *blocks = 1;
+  } else {
+    *kind = rows <= 128 || D == 256 ? 1 : 2;
+    *wk = 1;
+    *blocks = ceil_div(rows, 128 * *kind);
+  }
+}
 
-void split_keys(int keys, int base_blocks, int* chunk, int* parts) {
+void split_keys(int keys, int base_blocks, int want, int min_chunk, int* chunk, int* parts) {
   if (keys <= 0) {
-    *chunk = kAttnMinChunk, *parts = 0;
+    *chunk = min_chunk, *parts = 0;
     return;
   }
-  int p = kAttnBlocks / (base_blocks < 1 ? 1 : base_blocks);
-  const int most = ceil_div(keys, kAttnMinChunk);
+  int p = want / (base_blocks < 1 ? 1 : base_blocks);
+  const int most = ceil_div(keys, min_chunk);
   p = p < 1 ? 1 : p > most ? most : p;
   *chunk = ceil_div(ceil_div(keys, p), 128) * 128;
   *parts = ceil_div(keys, *chunk);
@@ -80,14 +96,12 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   a->n_pages = c->n_pages, a->page_shift = log2_of(c->page_size);
   a->prefix_len = prefix_len, a->max_keys = max_keys;
   a->fp8 = c->dtype == MOE_DT_FP8_E4M3;
-  const int rows_p = a->n_tok * a->G, rows_s = q_len * a->G;
-  a->prefix_rt = rows_p <= 16 ? 1 : 2;
-  a->own_rt = rows_s <= 16 ? 1 : 2;
-  a->prefix_blocks = ceil_div(rows_p, 16 * a->prefix_rt);
-  a->own_blocks = ceil_div(rows_s, 16 * a->own_rt);
-  split_keys(prefix_len, a->Hkv * a->prefix_blocks, &a->prefix_chunk, &a->n_prefix_parts);
+  split_rows(a->n_tok * a->G, a->D, &a->prefix_kind, &a->prefix_wk, &a->prefix_blocks);
+  split_rows(q_len * a->G, a->D, &a->own_kind, &a->own_wk, &a->own_blocks);
+  split_keys(prefix_len, a->Hkv * a->prefix_blocks, WANTP, MINP, &a->prefix_chunk,
+             &a->n_prefix_parts);
   split_keys(max_keys > prefix_len ? max_keys - (prefix_len & ~31) : 0,
-             a->B * a->Hkv * a->own_blocks, &a->own_chunk, &a->n_own_parts);
+             a->B * a->Hkv * a->own_blocks, WANTO, MINO, &a->own_chunk, &a->n_own_parts);
   const int64_t items = (int64_t)a->n_prefix_parts * a->Hkv * a->prefix_blocks +
                         (int64_t)a->n_own_parts * a->B * a->Hkv * a->own_blocks;
   if (items > 0x7fffffff) return MOE_ENOTSUP;
