@@ -27,6 +27,9 @@
 
 #include "common.h"
 #include "kernels.h"
+#ifndef PFN
+#define PFN 4
+#endif
 
 namespace bef {
 
@@ -162,17 +165,16 @@ __device__ __forceinline__ bool bad_key(const AttnArgs& a, const int32_t* pages,
   const int pg = pages[max(lo, min(j, hi - 1)) >> a.page_shift];
   return pg < 0 || pg >= a.n_pages;
 }
-// One block (4 waves) over the keys of rg for up to 64 rows, r0.. of `rows` (row
-// r is token t0 + r / G, query head h G + r % G).  The waves are 4 / wk row
-// sets of 16 rows by wk key sets: 32-key tiles are dealt out over the key sets,
-// whose sums are joined in LDS at the end.
+// One block (4 waves) over the keys of rg for RT x 16 rows, r0.. of `rows` (row r
+// is token t0 + r / G, query head h G + r % G): 32-key tiles are dealt out over
+// the waves, whose sums are joined in LDS at the end.
 //
 // A tile's K is dead once the scores are formed and its V once they are
 // multiplied, so the next tile's are loaded into the same registers right
 // then: a load has the rest of a tile's work to arrive in.
-template <int D, bool FP8>
+template <int D, bool FP8, int RT>
 __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int r0, int rows,
-                                          const Range& rg, int part, int wk, float* lds) {
+                                          const Range& rg, int part, float* lds) {
   constexpr int NS = D / 32;        // 32-column steps of the score product
   constexpr int VD = D / 16;        // columns per lane of V and O
   constexpr int ES = FP8 ? 1 : 2;
@@ -180,33 +182,44 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
   constexpr int VW = VD * ES / 4;            // dwords per key of this lane's V columns
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int kset = wv % wk, rset = wv / wk;
   const int slots = (1 << a.page_shift) - 1;
-  r0 += rset * 16;
 
-  // this lane's query, its operand and its limit.  Column order of the score
-  // product: bf16 K, step s of group g holds columns 32 s + 8 g; FP8 K, steps 2u
-  // and 2u+1 the halves of the 16 codes from 64 u + 16 g
-  const bool in = r0 + c < rows;
-  const int rr = min(r0 + c, rows - 1);
-  const int tok = t0 + rr / a.G, head = h * a.G + rr % a.G;
-  const int lim = in ? row_limit(a, tok) : 0;
-  const int maxlim = __builtin_amdgcn_readfirstlane(wave_max_all(lim));
-  const int minlim = __builtin_amdgcn_readfirstlane(wave_min_all(lim > 0 ? lim : 0x7fffffff));
-  uint4 q[NS];
-  {
+  // this lane's query of each row tile, its operand and its limit.  Column order of
+  // the score product: bf16 K, step s of group g holds columns 32 s + 8 g; FP8 K,
+  // steps 2u and 2u+1 the halves of the 16 codes from 64 u + 16 g
+  auto row_of = [&](int rt, int& tok, int& head) {
+    const int rr = min(r0 + 16 * rt + c, rows - 1);
+    tok = t0 + rr / a.G;
+    head = h * a.G + rr % a.G;
+    return r0 + 16 * rt + c < rows;
+  };
+  uint4 q[RT][NS];
+  int lim[RT], maxlim = 0, minlim = 0x7fffffff;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    int tok, head;
+    const bool in = row_of(rt, tok, head);
+    lim[rt] = in ? row_limit(a, tok) : 0;
+    maxlim = max(maxlim, lim[rt]);
+    minlim = min(minlim, lim[rt] > 0 ? lim[rt] : 0x7fffffff);
     const uint16_t* qr = a.q + (size_t)tok * a.q_stride + (size_t)head * D;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
-      q[s] = *reinterpret_cast<const uint4*>(
+      q[rt][s] = *reinterpret_cast<const uint4*>(
           qr + (FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g));
   }
+  maxlim = __builtin_amdgcn_readfirstlane(wave_max_all(maxlim));
+  minlim = __builtin_amdgcn_readfirstlane(wave_min_all(minlim));
   const int lo = rg.lo, hi = min(rg.hi, maxlim);
 
-  v4f_t o[VD];
-  float m = -INFINITY, l = 0.0f;
+  v4f_t o[RT][VD];
+  float m[RT], l[RT];
 #pragma unroll
-  for (int j = 0; j < VD; ++j) o[j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY, l[rt] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VD; ++j) o[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  }
   float vref = 0.0f;  // FP8: o is in units of this power of two
 
   // the 16-key halves' first cache rows (the second half may lie past the last
@@ -295,7 +308,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     }
 
     // scores
-    float x[8];
+    float x[RT][8];
     {
       uint4 kf[2][NS];
 #pragma unroll
@@ -309,14 +322,17 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
             kf[u][s] = kr[u][s];
           }
         }
-      v4f_t s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        s0 = mfma(kf[0][s], q[s], s0);
-        s1 = mfma(kf[1][s], q[s], s1);
+      for (int rt = 0; rt < RT; ++rt) {
+        v4f_t s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          s0 = mfma(kf[0][s], q[rt][s], s0);
+          s1 = mfma(kf[1][s], q[rt][s], s1);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[rt][e] = s0[e], x[rt][4 + e] = s1[e];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = s0[e], x[4 + e] = s1[e];
     }
     float vscale[8];
     if constexpr (FP8) {
@@ -326,7 +342,8 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
         const float vv[4] = {vs4[u].x, vs4[u].y, vs4[u].z, vs4[u].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[4 * u + e] *= kk[e];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) x[rt][4 * u + e] *= kk[e];
           vscale[4 * u + e] = vv[e];
         }
       }
@@ -348,7 +365,9 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
       }
       raise_vref(vm, vref, [&](float f) {
 #pragma unroll
-        for (int j = 0; j < VD; ++j) o[j] *= f;
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int j = 0; j < VD; ++j) o[rt][j] *= f;
       });
       const float inv = 1.0f / vref;
 #pragma unroll
@@ -356,25 +375,30 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     }
 
     // probabilities
-    if (edge) {
+    uint4 p[RT];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!inside(e) || key_of(e) >= lim) x[e] = -INFINITY;
+    for (int rt = 0; rt < RT; ++rt) {
+      if (edge) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!inside(e) || key_of(e) >= lim[rt]) x[rt][e] = -INFINITY;
+      }
+      raise_max(max8(x[rt]) * a.scale_log2, m[rt], [&](float f) {
+        l[rt] *= f;
+#pragma unroll
+        for (int j = 0; j < VD; ++j) o[rt][j] *= f;
+      });
+      const float mu = m[rt] == -INFINITY ? 0.0f : m[rt];
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        w[e] = __builtin_amdgcn_exp2f(fmaf(x[rt][e], a.scale_log2, -mu));
+        l[rt] += w[e];
+        // (0 x a non-finite scale: only in tiles set aside)
+        if (FP8) w[e] = SLOW && x[rt][e] == -INFINITY ? 0.0f : w[e] * vscale[e];
+      }
+      p[rt] = pack_p<FP8>(w);
     }
-    raise_max(max8(x) * a.scale_log2, m, [&](float f) {
-      l *= f;
-#pragma unroll
-      for (int j = 0; j < VD; ++j) o[j] *= f;
-    });
-    const float mu = m == -INFINITY ? 0.0f : m;
-    float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale_log2, -mu));
-      l += w[e];
-      if (FP8) w[e] = edge && x[e] == -INFINITY ? 0.0f : w[e] * vscale[e];
-    }
-    const uint4 p = pack_p<FP8>(w);
 
     // O^T += V^T P^T, column set j of the lanes
     auto v_operand = [&](int j) -> uint4 {
@@ -397,10 +421,18 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     };
     if constexpr (!SLOW) {
 #pragma unroll
-      for (int j = 0; j < VD; ++j) o[j] = mfma_pv<FP8>(v_operand(j), p, o[j]);
+      for (int j = 0; j < VD; ++j) {
+        const uint4 vf = v_operand(j);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
+      }
     } else {
       for (int done = -1;;) {
-        const int next = wave_min_all(lim > done ? lim : 0x7fffffff);
+        int next = 0x7fffffff;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          if (lim[rt] > done) next = min(next, lim[rt]);
+        next = wave_min_all(next);
         if (next == 0x7fffffff) break;
         done = next;
 #pragma unroll
@@ -411,8 +443,12 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
           for (int i = 0; i < 4; ++i)
             d[i] &= (key_of(2 * i) < done ? 0xffffu : 0u) |
                     (key_of(2 * i + 1) < done ? 0xffff0000u : 0u);
-          const v4f_t n = mfma_pv<FP8>(make_uint4(d[0], d[1], d[2], d[3]), p, o[j]);
-          if (lim == done) o[j] = n;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const v4f_t n = mfma_pv<FP8>(make_uint4(d[0], d[1], d[2], d[3]), p[rt], o[rt][j]);
+            if (lim[rt] == done) o[rt][j] = n;
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
@@ -420,7 +456,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     return true;
   };
 
-  const int step = 32 * wk, first = (lo & ~31) + 32 * kset;
+  const int step = 128, first = (lo & ~31) + 32 * wv;
   bool leaked = false;
   {
     Rows cur{}, nxt{};
@@ -448,52 +484,55 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     }
   }
 
-  // the key sets' sums joined through LDS, in halves
-  l = quad_sum(l);
+  // the waves' sums joined through LDS, in halves, a row tile at a time
   float2* lml = reinterpret_cast<float2*>(lds);  // [wave][64]: m, l
   float* lo_ = lds + 4 * 64 * 2;                 // [2][VD * 4][64]
-  float f = FP8 ? vref : 1.0f;
-  if (wk > 1) {
-    lml[wv * 64 + lane] = make_float2(m, l);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    lml[wv * 64 + lane] = make_float2(m[rt], quad_sum(l[rt]));
     __syncthreads();
     float M = -INFINITY, L = 0.0f;
-    for (int w = rset * wk; w < (rset + 1) * wk; ++w) M = fmaxf(M, lml[w * 64 + lane].x);
-    for (int w = rset * wk; w < (rset + 1) * wk; ++w) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, lml[w * 64 + lane].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
       const float2 ml = lml[w * 64 + lane];
       if (ml.x != -INFINITY) L += ml.y * __builtin_amdgcn_exp2f(ml.x - M);
     }
-    f = m == -INFINITY ? 0.0f : f * __builtin_amdgcn_exp2f(m - M);
-    m = M, l = L;
-  }
+    const float f =
+        (FP8 ? vref : 1.0f) * (m[rt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[rt] - M));
 #pragma unroll
-  for (int j = 0; j < VD; ++j) o[j] *= f;
-  for (int half = wk >> 1; half > 0; half >>= 1) {
-    float* mine = lo_ + (rset * half + kset % half) * (VD * 4 * 64) + lane;
-    if (kset >= half && kset < 2 * half) {
+    for (int j = 0; j < VD; ++j) o[rt][j] *= f;
 #pragma unroll
-      for (int j = 0; j < VD; ++j)
+    for (int half = 2; half > 0; half >>= 1) {
+      float* mine = lo_ + (wv % half) * (VD * 4 * 64) + lane;
+      if (wv >= half && wv < 2 * half) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mine[(j * 4 + r) * 64] = o[j][r];
+        for (int j = 0; j < VD; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) mine[(j * 4 + r) * 64] = o[rt][j][r];
+      }
+      __syncthreads();
+      if (wv < half) {
+#pragma unroll
+        for (int j = 0; j < VD; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[rt][j][r] += mine[(j * 4 + r) * 64];
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (kset < half) {
+    int tok, head;
+    if (wv || !row_of(rt, tok, head)) continue;
+    const size_t row = ((size_t)part * a.n_tok + tok) * a.Hq + head;
+    if (g == 0) a.pml[row] = make_float2(lim[rt] ? M : -INFINITY, lim[rt] ? L : 0.0f);
+    float* dst = a.po + row * D + VD * 4 * g;
 #pragma unroll
-      for (int j = 0; j < VD; ++j)
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[j][r] += mine[(j * 4 + r) * 64];
-    }
-    __syncthreads();
+      for (int j = 0; j < VD; j += 4)
+        *reinterpret_cast<float4*>(dst + VD * r + j) =
+            make_float4(o[rt][j][r], o[rt][j + 1][r], o[rt][j + 2][r], o[rt][j + 3][r]);
   }
-  if (kset || !in) return;
-  const size_t row = ((size_t)part * a.n_tok + tok) * a.Hq + head;
-  if (g == 0) a.pml[row] = make_float2(lim ? m : -INFINITY, lim ? l : 0.0f);
-  float* dst = a.po + row * D + VD * 4 * g;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int j = 0; j < VD; j += 4)
-      *reinterpret_cast<float4*>(dst + VD * r + j) =
-          make_float4(o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]);
 }
 
 // The keys that the longest-sighted of sequence b's tokens sees (wave-uniform).
@@ -513,7 +552,7 @@ __device__ __forceinline__ int own_parts(const AttnArgs& a, int lim) {
 // An item of the grid: a range of keys for one kv head and a block of rows.
 struct Item {
   Range rg;
-  int h, t0, rows, rb, part, wk;
+  int h, t0, rows, rb, part;
 };
 
 // The first `np` items are the prefix's, the others the sequences' own; false
@@ -533,7 +572,7 @@ __device__ __forceinline__ bool item_of(const AttnArgs& a, int item, int np, Ite
       pair = item / a.prefix_blocks;
     }
     it.rb = rb, it.h = pair % a.Hkv, it.part = pair / a.Hkv;
-    it.t0 = 0, it.rows = a.n_tok * a.G, it.wk = a.prefix_wk;
+    it.t0 = 0, it.rows = a.n_tok * a.G;
     it.rg = {a.prefix_pages, it.part * a.prefix_chunk,
              min((it.part + 1) * a.prefix_chunk, a.prefix_len)};
     return true;
@@ -546,18 +585,23 @@ __device__ __forceinline__ bool item_of(const AttnArgs& a, int item, int np, Ite
   const int b = item % a.B, part = item / a.B;
   if (part >= own_parts(a, seq_limit(a, b))) return false;
   const int base = (a.prefix_len & ~31) + part * a.own_chunk;
-  it.t0 = b * a.Q, it.rows = a.Q * a.G, it.wk = a.own_wk, it.part = a.n_prefix_parts + part;
+  it.t0 = b * a.Q, it.rows = a.Q * a.G, it.part = a.n_prefix_parts + part;
   it.rg = {a.table + (size_t)b * a.table_cols, max(base, a.prefix_len),
            min(base + a.own_chunk, a.max_keys)};
   return true;
 }
 
-template <int D, bool FP8>
-__global__ __launch_bounds__(256, D < 256 ? 3 : 2) void attn_part_kernel(AttnArgs a, int np) {
+// RTP, RTS: row tiles of a block of the prefix's and of the sequences' own items.
+template <int D, bool FP8, int RTP, int RTS>
+__global__ __launch_bounds__(256, D < 256 && RTP == 1 ? 3 : 2) void attn_part_kernel(AttnArgs a,
+                                                                                    int np) {
   __shared__ __align__(8) float lds[4 * 64 * 2 + 2 * (D / 16) * 4 * 64];
   Item it;
   if (!item_of(a, blockIdx.x, np, it)) return;
-  attn_item<D, FP8>(a, it.h, it.t0, it.rb * 16 * (4 / it.wk), it.rows, it.rg, it.part, it.wk, lds);
+  if (RTP == RTS || (int)blockIdx.x < np)
+    attn_item<D, FP8, RTP>(a, it.h, it.t0, it.rb * 16 * RTP, it.rows, it.rg, it.part, lds);
+  else
+    attn_item<D, FP8, RTS>(a, it.h, it.t0, it.rb * 16 * RTS, it.rows, it.rg, it.part, lds);
 }
 
 // ---- many rows: keys staged in LDS for eight waves of rows -------------------
@@ -575,7 +619,8 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
   constexpr int CH = D / 8;                       // 16-byte chunks of an LDS K row
   __shared__ uint4 lk[2][64][CH];
   __shared__ uint4 lv[2][D][8];                   // [column][8 chunks of 8 key slots]
-  __shared__ float lks[2][64], lvs[2][64];
+  // FP8: K scales; V scales in units of lvref, a power of two that bounds all so far
+  __shared__ float lks[2][64], lvs[2][64], lvref[2];
   // marks by buffer: the tile (its first key) that holds a non-finite V, a bad page;
   // whether a wave has set a group aside
   __shared__ int lleak[2], lbad[2], lslow;
@@ -620,7 +665,9 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
 #pragma unroll
     for (int j = 0; j < VD; ++j) o[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
   }
-  float vref = 0.0f;
+  // P v_scale enters the product in fp16: o in units of a power of two that bounds
+  // the scales, so that it stays small (`bound`: wave 1's, which stages them)
+  float vref = 0.0f, bound = 0x1p-100f;
 
   // this thread's pieces of a tile: K piece i is 16 bytes of key kkey + i x
   // (keys per round); V unit i is columns 8 vcol.. of keys 2 vkp, 2 vkp + 1
@@ -738,14 +785,16 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
           reinterpret_cast<uint32_t*>(&lv[buf][d][swz_v(d, slot >> 3)])[(slot & 7) >> 1] = two;
         }
       }
-    if (FP8 && tid < 128) {
-      const bool ok = okbits >> 31;
-      if (tid < 64) {
-        lks[buf][tid] = sreg;
-      } else {
-        lvs[buf][tid & 63] = ok ? sreg : 0.0f;
-        leak |= ok && !(fabsf(sreg) < INFINITY);
-      }
+    if (FP8 && wv == 0) lks[buf][lane] = sreg;
+    if (FP8 && wv == 1) {
+      const float v = okbits >> 31 ? sreg : 0.0f;
+      const bool finite = fabsf(v) < INFINITY;
+      leak |= !finite;
+      const float vm =
+          __uint_as_float(__float_as_uint(wave_max(finite ? fabsf(v) : 0.0f)) & 0x7f800000u);
+      bound = fmaxf(bound, vm + vm);
+      lvs[buf][lane] = v / bound;
+      if (lane == 0) lvref[buf] = bound;
     }
     if (leak) lleak[buf] = j0;
     if (badp) lbad[buf] = j0;
@@ -812,7 +861,6 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
       }
       float vscale[8];
       if constexpr (FP8) {
-        float vm = 0.0f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const float4 kk = *reinterpret_cast<const float4*>(&lks[buf][32 * kt + 16 * u + 4 * g]);
@@ -823,19 +871,28 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) x[kb][rt][4 * u + e] *= k4[e];
             vscale[4 * u + e] = v4[e];
-            vm = fmaxf(vm, fabsf(v4[e]) < INFINITY ? fabsf(v4[e]) : 0.0f);
           }
         }
-        raise_vref(vm, vref, [&](float f) {
+        const float nref =
+            __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(lvref[buf])));
+        if (nref != vref) {
+          const float f = vref / nref;
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int j = 0; j < VD; ++j) o[rt][j] *= f;
-        });
-        const float inv = 1.0f / vref;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) vscale[e] *= inv;
+          vref = nref;
+        }
       }
+      auto v_operand = [&](int j) {
+        const int d = 16 * j + c;
+        return lv[buf][d][swz_v(d, 4 * kt + g)];
+      };
+      // the first V operands arrive under the softmax
+      constexpr int VPF = PFN;
+      uint4 va[VPF];
+#pragma unroll
+      for (int j = 0; j < VPF; ++j) va[j] = v_operand(j);
       uint4 p[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
@@ -857,18 +914,15 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
         for (int e = 0; e < 8; ++e) {
           w[e] = __builtin_amdgcn_exp2f(fmaf(x[kb][rt][e], a.scale_log2, -mu));
           l[rt] += w[e];
-          if (FP8) w[e] = edge && x[kb][rt][e] == -INFINITY ? 0.0f : w[e] * vscale[e];
+          // (0 x a non-finite scale: only in groups set aside)
+          if (FP8) w[e] = SLOW && x[kb][rt][e] == -INFINITY ? 0.0f : w[e] * vscale[e];
         }
         p[rt] = pack_p<FP8>(w);
       }
-      auto v_operand = [&](int j) {
-        const int d = 16 * j + c;
-        return lv[buf][d][swz_v(d, 4 * kt + g)];
-      };
       if constexpr (!SLOW) {
 #pragma unroll
         for (int j = 0; j < VD; ++j) {
-          const uint4 vf = v_operand(j);
+          const uint4 vf = j < VPF ? va[j % VPF] : v_operand(j);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
         }
@@ -999,23 +1053,31 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 
 namespace {
 
-// Both sorts of item in one launch where they are of one kind (AttnArgs).
-template <int D, bool FP8, int KIND>
-void launch_parts(const AttnArgs& a, hipStream_t st) {
-  const int np = a.prefix_kind == KIND ? a.n_prefix_parts * a.Hkv * a.prefix_blocks : 0;
-  const int no = a.own_kind == KIND ? a.n_own_parts * a.B * a.Hkv * a.own_blocks : 0;
-  if (np + no == 0) return;
-  if constexpr (KIND == 0)
-    attn_part_kernel<D, FP8><<<np + no, 256, 0, st>>>(a, np);
-  else
-    attn_tile_kernel<D, FP8, KIND><<<np + no, 512, 0, st>>>(a, np);
+// Items whose blocks take few rows (AttnArgs kinds 1, 2), both sorts in one launch.
+template <int D, bool FP8>
+void launch_few(const AttnArgs& a, int np, int no, hipStream_t st) {
+  const bool p2 = np && a.prefix_kind == 2, s2 = no && a.own_kind == 2;
+  if constexpr (D < 256) {
+    if (p2 && !s2 && no) {
+      attn_part_kernel<D, FP8, 2, 1><<<np + no, 256, 0, st>>>(a, np);
+      return;
+    }
+    if (p2 || s2) {  // (where both are there, the prefix's rows are the more)
+      attn_part_kernel<D, FP8, 2, 2><<<np + no, 256, 0, st>>>(a, np);
+      return;
+    }
+  }
+  attn_part_kernel<D, FP8, 1, 1><<<np + no, 256, 0, st>>>(a, np);
 }
 
 template <int D, bool FP8>
 void launch_dim(const AttnArgs& a, hipStream_t st) {
-  launch_parts<D, FP8, 1>(a, st);
-  if constexpr (D < 256) launch_parts<D, FP8, 2>(a, st);
-  launch_parts<D, FP8, 0>(a, st);
+  const int np = a.n_prefix_parts * a.Hkv * a.prefix_blocks;
+  const int no = a.n_own_parts * a.B * a.Hkv * a.own_blocks;
+  constexpr int RT = D == 256 ? 1 : 2;
+  const int tp = a.prefix_kind == kAttnTile ? np : 0, ts = a.own_kind == kAttnTile ? no : 0;
+  if (tp + ts) attn_tile_kernel<D, FP8, RT><<<tp + ts, 512, 0, st>>>(a, tp);
+  if (np + no > tp + ts) launch_few<D, FP8>(a, np - tp, no - ts, st);
 }
 
 template <int D>

@@ -198,6 +198,7 @@ struct LogprobArgs {
 hipError_t launch_logprobs(const LogprobArgs& a, bool bf16, hipStream_t st);
 
 // Shared-prefix attention (attn.hip).
+constexpr int kAttnTile = 3;
 struct AttnArgs {
   const void *k, *v;
   const float *ks, *vs;
@@ -213,12 +214,11 @@ struct AttnArgs {
   int B, Q, n_tok, Hq, Hkv, G, D;
   int table_cols, n_pages, page_shift, prefix_len, max_keys;
   bool fp8;
-  // split of the prefix's items and of the sequences' own: kind (0: 16 rows a
-  // wave, keys straight to registers; 1, 2: 16 x kind rows, keys through LDS),
-  // wk (kind 0: key sets that a block's 4 waves form, the rest are row sets),
-  // row blocks, keys per part, parts
-  int prefix_kind, prefix_wk, prefix_blocks, prefix_chunk, n_prefix_parts;
-  int own_kind, own_wk, own_blocks, own_chunk, n_own_parts;
+  // split of the prefix's items and of the sequences' own: kind (1, 2: blocks of
+  // 16 x kind rows, keys straight to registers; kAttnTile: of 256 rows, 128 at 256
+  // columns, keys through LDS), row blocks, keys per part, parts
+  int prefix_kind, prefix_blocks, prefix_chunk, n_prefix_parts;
+  int own_kind, own_blocks, own_chunk, n_own_parts;
 };
 hipError_t launch_attn(const AttnArgs& a, hipStream_t st);
 

@@ -9,13 +9,6 @@
 #include "moe.h"
 
 using namespace bef;
-#ifndef WANTP
-#define WANTP 256
-#define MINP 256
-#define WANTO 1024
-#define MINO 256
-#endif
-
 namespace {
 
 constexpr int kMaxT = 1 << 18;
@@ -55,26 +48,32 @@ int check_rows(int64_t stride, int64_t n) {
 // ---- attention: how the work is split ---------------------------------------
 namespace {
 
-// How `rows` query rows of a kv head are taken (see AttnArgs).
-void split_rows(int rows, int D, int* kind, int* wk, int* blocks) {
-  if (rows <= 64) {
-    *kind = 0;
-    *wk = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;
-    *blocks = 1;
+// How `rows` query rows of a kv head are taken (see AttnArgs).  Measured at 128
+// columns over 8192 shared keys: blocks of 16 rows up to 64 (32 rows: 16.0 us, 18.9 in
+// blocks of 32), of 32 rows up to 128 (128 rows: 23.7 us, 29.0 in blocks of 16, whose
+// repeated reads of K and V L2 then bounds), keys through LDS above (512 rows over
+// 32768 keys: 114 us, 189 in blocks of 32).
+void split_rows(int rows, int D, int* kind, int* blocks) {
+  if (rows <= 128) {
+    *kind = rows <= 64 || D == 256 ? 1 : 2;
+    *blocks = ceil_div(rows, 16 * *kind);
   } else {
-    *kind = rows <= 128 || D == 256 ? 1 : 2;
-    *wk = 1;
-    *blocks = ceil_div(rows, 128 * *kind);
+    *kind = kAttnTile;
+    *blocks = ceil_div(rows, D == 256 ? 128 : 256);
   }
 }
 
-void split_keys(int keys, int base_blocks, int want, int min_chunk, int* chunk, int* parts) {
-  if (keys <= 0) {
-    *chunk = min_chunk, *parts = 0;
-    return;
-  }
-  int p = want / (base_blocks < 1 ? 1 : base_blocks);
-  const int most = ceil_div(keys, min_chunk);
+// Keys per part (a multiple of 128) and parts, for about `want` blocks.  A part has
+// 256 keys at least (its sums are written and read again), or 128 where the chip
+// would not even get a block per CU.
+void split_keys(int keys, int kind, int base_blocks, int want, int* chunk, int* parts) {
+  *chunk = 128, *parts = 0;
+  if (keys <= 0) return;
+  if (base_blocks < 1) base_blocks = 1;
+  const int least =
+      kind != kAttnTile && keys <= 4096 && (int64_t)base_blocks * ceil_div(keys, 256) < 256 ? 128 : 256;
+  const int most = ceil_div(keys, least);
+  int p = want / base_blocks;
   p = p < 1 ? 1 : p > most ? most : p;
   *chunk = ceil_div(ceil_div(keys, p), 128) * 128;
   *parts = ceil_div(keys, *chunk);
@@ -96,12 +95,20 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   a->n_pages = c->n_pages, a->page_shift = log2_of(c->page_size);
   a->prefix_len = prefix_len, a->max_keys = max_keys;
   a->fp8 = c->dtype == MOE_DT_FP8_E4M3;
-  split_rows(a->n_tok * a->G, a->D, &a->prefix_kind, &a->prefix_wk, &a->prefix_blocks);
-  split_rows(q_len * a->G, a->D, &a->own_kind, &a->own_wk, &a->own_blocks);
-  split_keys(prefix_len, a->Hkv * a->prefix_blocks, WANTP, MINP, &a->prefix_chunk,
-             &a->n_prefix_parts);
-  split_keys(max_keys > prefix_len ? max_keys - (prefix_len & ~31) : 0,
-             a->B * a->Hkv * a->own_blocks, WANTO, MINO, &a->own_chunk, &a->n_own_parts);
+  split_rows(a->n_tok * a->G, a->D, &a->prefix_kind, &a->prefix_blocks);
+  split_rows(q_len * a->G, a->D, &a->own_kind, &a->own_blocks);
+  const int base_p = a->Hkv * a->prefix_blocks;
+  // blocks wanted: a prefix one per CU, all together four per CU (half of each at
+  // 256 columns, whose blocks take twice the registers)
+  const int want_p = a->D == 256 ? 128 : 256, want = 4 * want_p;
+  split_keys(prefix_len, a->prefix_kind, base_p,
+             a->prefix_kind == kAttnTile ? 256 : want_p, &a->prefix_chunk, &a->n_prefix_parts);
+  const int taken = a->prefix_kind != kAttnTile && a->own_kind != kAttnTile
+                        ? base_p * a->n_prefix_parts
+                        : 0;
+  split_keys(max_keys > prefix_len ? max_keys - (prefix_len & ~31) : 0, a->own_kind,
+             a->B * a->Hkv * a->own_blocks, want - taken < want_p ? want_p : want - taken,
+             &a->own_chunk, &a->n_own_parts);
   const int64_t items = (int64_t)a->n_prefix_parts * a->Hkv * a->prefix_blocks +
                         (int64_t)a->n_own_parts * a->B * a->Hkv * a->own_blocks;
   if (items > 0x7fffffff) return MOE_ENOTSUP;
