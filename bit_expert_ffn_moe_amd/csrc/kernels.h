@@ -188,6 +188,7 @@ struct LogprobArgs {
   const void* z;
   int64_t row_stride;
   int T, V, W, n_top;
+  bool by_row;                  // one block per row: no partials
   const int32_t* tokens;
   float *logprob, *entropy, *top_logprobs;
   int32_t* top_ids;

@@ -4,12 +4,15 @@
 //   H = log l - sum (z-M) e^(z-M) / l,  best n by (z descending, id ascending).
 //
 // One pass over the logits.  A wave takes 2048 consecutive elements into
-// registers (32 a lane), forms its own maximum and sums there, and selects its
-// n best: its lanes' best elements are sorted across the wave, which bounds the
-// n-th best from below; lanes whose next element still beats that bound
-// offer it, until none does.  Partials (m, l, sum, n keys) go to the
-// workspace; a second kernel joins a row's waves.  HBM-bound when there are many
-// rows, latency-bound for one.
+// registers (32 a lane) and forms its maximum and sums there.  Its n best: the
+// n-th largest of the lanes' maxima bounds the n-th best from below, so the
+// few elements that reach it are collected and sorted across the wave.
+//   Few rows: a wave per 2048 elements leaves (m, l, sum, n keys) in the workspace
+// and a second kernel joins a row's waves: latency-bound.
+//   Many rows: a block of four waves walks a row, each wave keeping its statistics and
+// its n best so far (later elements then mostly fall short of its n-th best), and
+// joins them itself: bound by HBM and, closely, by the vector unit (an
+// exponential and ten more operations an element).
 //
 // A candidate is one 64-bit key: the logit's order in the high word (a
 // monotone map of fp32 to unsigned, NaN 1 and below every number, 0 for places
@@ -37,9 +40,29 @@ __device__ __forceinline__ float order_value(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
 
-__device__ __forceinline__ u64 shfl_xor64(u64 v, int m) {
-  const uint32_t lo = __shfl_xor((uint32_t)v, m), hi = __shfl_xor((uint32_t)(v >> 32), m);
-  return (u64)hi << 32 | lo;
+// The value of lane l ^ J: DPP inside rows of 16 (4 as mirror of 8, then of 4), row
+// swaps across them.
+template <int J>
+__device__ __forceinline__ uint32_t exch(uint32_t v) {
+  if constexpr (J == 1) {
+    return dpp_row<0xB1>((int)v);
+  } else if constexpr (J == 2) {
+    return dpp_row<0x4E>((int)v);
+  } else if constexpr (J == 4) {
+    return dpp_row<0x1B>(dpp_row<0x141>((int)v));
+  } else if constexpr (J == 8) {
+    return dpp_row<0x128>((int)v);  // row_ror:8
+  } else if constexpr (J == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16) ? r[0] : r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (threadIdx.x & 32) ? r[0] : r[1];
+  }
+}
+template <int J>
+__device__ __forceinline__ u64 exch(u64 v) {
+  return (u64)exch<J>((uint32_t)(v >> 32)) << 32 | exch<J>((uint32_t)v);
 }
 __device__ __forceinline__ u64 lane64(u64 v, int l) {
   const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, l);
@@ -47,29 +70,65 @@ __device__ __forceinline__ u64 lane64(u64 v, int l) {
   return (u64)hi << 32 | lo;
 }
 
-// Bitonic sort over the wave, largest key in lane 0.
-__device__ __forceinline__ u64 wave_sort(u64 v, int lane) {
-#pragma unroll
-  for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const u64 o = shfl_xor64(v, j);
-      const bool keep_max = ((lane & j) == 0) == ((lane & k) == 0);
-      v = (v > o) == keep_max ? v : o;
-    }
+// One step of a bitonic network over the wave: pairs (l, l ^ J), the larger to
+// the lane where `first` says so.
+template <int J, class T>
+__device__ __forceinline__ T step(T v, bool first) {
+  const T o = exch<J>(v);
+  return (v > o) == first ? v : o;
+}
+// Sorts runs of K, falling where lane & K is 0 (everywhere for K = 64).
+template <int K, int J, class T>
+__device__ __forceinline__ T clean(T v, int lane) {
+  v = step<J>(v, ((lane & J) == 0) == ((lane & K) == 0));
+  if constexpr (J > 1) v = clean<K, J / 2>(v, lane);
   return v;
+}
+// Bitonic sort over the wave, largest in lane 0 (unsigned values).
+template <int K = 2, class T>
+__device__ __forceinline__ T wave_sort(T v, int lane) {
+  v = clean<K, K / 2>(v, lane);
+  if constexpr (K < 64) v = wave_sort<2 * K>(v, lane);
+  return v;
+}
+
+__device__ __forceinline__ u64 larger(u64 a, u64 b) { return a > b ? a : b; }
+__device__ __forceinline__ u64 wave_largest(u64 v) {
+  v = larger(v, exch<1>(v));
+  v = larger(v, exch<2>(v));
+  v = larger(v, exch<4>(v));
+  v = larger(v, exch<8>(v));
+  v = larger(v, exch<16>(v));
+  return larger(v, exch<32>(v));
 }
 
 // The 64 largest of two sorted lists, sorted.
 __device__ __forceinline__ u64 wave_merge(u64 a, u64 b, int lane) {
-  const u64 r = shfl_xor64(b, 63);
-  u64 v = a > r ? a : r;
+  // b turned round: lane l ^ 63
+  u64 r = exch<32>(exch<16>(b));
+  r = (u64)(uint32_t)dpp_row<0x140>((int)(r >> 32)) << 32 | (uint32_t)dpp_row<0x140>((int)r);
+  return clean<64, 32>(a > r ? a : r, lane);
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float max_of(const float (&z)[kPerLane]) {
+  float m = z[0];
 #pragma unroll
-  for (int j = 32; j > 0; j >>= 1) {
-    const u64 o = shfl_xor64(v, j);
-    v = (v > o) == ((lane & j) == 0) ? v : o;
+  for (int i = 1; i < kPerLane; ++i) m = fmaxf(m, z[i]);
+  return m;
+}
+
+// Adds a part (m, l, s) to sums relative to M >= m.
+__device__ __forceinline__ void add_part(float m, float li, float si, float M, float& l,
+                                         float& s) {
+  if (m == -INFINITY) {
+    l += li;  // 0, or NaN where the part held nothing but NaN and -inf
+    return;
   }
-  return v;
+  const float d = (m - M) * kLog2e, f = __builtin_amdgcn_exp2f(d);
+  l = fmaf(f, li, l);
+  s = fmaf(f, fmaf(d, li, si), s);
 }
 
 template <bool BF16>
@@ -80,186 +139,380 @@ __device__ __forceinline__ float load_z(const void* row, int64_t i) {
 
 }  // namespace
 
-// grid (T, ceil(W / 4)): wave = one chunk of one row.
+namespace {
+
+// A row as aligned 16-byte words: `base` is its address rounded down, `off`
+// its first element's place there.  Nothing before the row's first element or
+// after its last is read.
+struct Row {
+  const uint8_t* base;
+  int off, end;  // elements [off, end)
+};
 template <bool BF16>
-__global__ __launch_bounds__(256) void logprob_chunk_kernel(LogprobArgs a) {
-  constexpr int VE = BF16 ? 8 : 4, NV = kPerLane / VE, ES = BF16 ? 2 : 4;
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x, w = blockIdx.y * 4 + (threadIdx.x >> 6);
-  if (w >= a.W) return;
+__device__ __forceinline__ Row row_of(const LogprobArgs& a, int t) {
+  constexpr int ES = BF16 ? 2 : 4;
   const uint8_t* row = (const uint8_t*)a.z + (size_t)t * a.row_stride * ES;
-  // 16-byte words from the row's address rounded down; the elements before the
-  // row's first and after its last are not read
-  const int off = (int)((uintptr_t)row & 15) / ES;
-  const uint8_t* base = row - off * ES;
-  float z[kPerLane];
-  const int e0 = w * kLogprobChunk + lane * VE;
+  Row r;
+  r.off = (int)((uintptr_t)row & 15) / ES;
+  r.base = row - r.off * ES;
+  r.end = r.off + a.V;
+  return r;
+}
+
+// Place of element i of this lane in chunk w.
+template <bool BF16>
+__device__ __forceinline__ int place(int w, int lane, int i) {
+  constexpr int VE = BF16 ? 8 : 4;
+  return w * kLogprobChunk + ((i / VE) * 64 + lane) * VE + i % VE;
+}
+
+// Chunk w's raw words (whole ones; others are read element by element in unpack).
+constexpr int kMaxWords = kPerLane / 4;
+template <bool BF16>
+__device__ __forceinline__ void load_chunk(const Row& r, int w, int lane,
+                                           uint4 (&raw)[kMaxWords]) {
+  constexpr int VE = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = e0 + v * 64 * VE;
-    if (e >= off && e + VE <= off + a.V) {
-      const uint4 r = *reinterpret_cast<const uint4*>(base + (size_t)e * ES);
-      const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+  for (int v = 0; v < kPerLane / VE; ++v) {
+    const int e = place<BF16>(w, lane, v * VE);
+    if (e >= r.off && e + VE <= r.end)
+      raw[v] = *reinterpret_cast<const uint4*>(r.base + (size_t)e * ES);
+  }
+}
+// ... as fp32, -inf outside the row.
+template <bool BF16>
+__device__ __forceinline__ void unpack_chunk(const Row& r, int w, int lane,
+                                             const uint4 (&raw)[kMaxWords],
+                                             float (&z)[kPerLane]) {
+  constexpr int VE = BF16 ? 8 : 4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (BF16) {
-          z[v * VE + 2 * i] = __uint_as_float(x[i] << 16);
-          z[v * VE + 2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
-        } else {
-          z[v * VE + i] = __uint_as_float(x[i]);
-        }
+  for (int v = 0; v < kPerLane / VE; ++v) {
+    const uint32_t x[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      z[v * VE + i] = BF16 ? __uint_as_float((i & 1) ? x[i / 2] & 0xffff0000u : x[i / 2] << 16)
+                           : __uint_as_float(x[i % 4]);
+  }
+  if (w * kLogprobChunk < r.off || (w + 1) * kLogprobChunk > r.end) {
+#pragma unroll
+    for (int v = 0; v < kPerLane / VE; ++v) {
+      const int e = place<BF16>(w, lane, v * VE);
+      if (!(e >= r.off && e + VE <= r.end)) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          z[v * VE + i] = e + i >= r.off && e + i < r.end ? load_z<BF16>(r.base, e + i) : -INFINITY;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-        z[v * VE + i] = (e + i >= off && e + i < off + a.V) ? load_z<BF16>(base, e + i) : -INFINITY;
     }
   }
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) m = fmaxf(m, z[i]);
-  m = wave_max(m);
-  const float mu = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const float d = z[i] - mu, e = __expf(d);
-    l += e;
-    s = fmaf(fmaxf(d, -1e30f), e, s);  // -inf contributes 0; NaN stays in e
-  }
-  l = wave_sum_dpp(l);
-  s = wave_sum_dpp(s);
-  const size_t part = (size_t)t * a.W + w;
-  if (lane == 0) {
-    a.pm[part] = m;
-    a.pl[part] = l;
-    a.ps[part] = s;
-  }
-  if (a.n_top == 0) return;
+}
 
+// Running statistics of a lane: maximum m (of the wave), l = sum 2^t and
+// s = sum t 2^t with t = (z - m) log2 e; t of -inf counts as -1e30 in s, where its
+// weight is 0.  A NaN or +inf makes l NaN.
+struct Stats {
+  float m, l, s;
+};
+__device__ __forceinline__ void add_chunk(const float (&z)[kPerLane], float lane_max, Stats& st) {
+  const float m = fmaxf(st.m, wave_max(lane_max));
+  if (m > st.m) {
+    if (st.m != -INFINITY) {
+      const float d = (st.m - m) * kLog2e, f = __builtin_amdgcn_exp2f(d);
+      st.s = f * fmaf(d, st.l, st.s);
+      st.l *= f;
+    }
+    st.m = m;
+  }
+  const float c = st.m == -INFINITY ? 0.0f : -st.m * kLog2e;
+  // two sums each: shorter chains
+  float l0 = 0.0f, l1 = 0.0f, s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPerLane; i += 2) {
+    const float t0 = fmaf(z[i], kLog2e, c), t1 = fmaf(z[i + 1], kLog2e, c);
+    const float e0 = __builtin_amdgcn_exp2f(t0), e1 = __builtin_amdgcn_exp2f(t1);
+    l0 += e0, l1 += e1;
+    s0 = fmaf(fmaxf(t0, -1e30f), e0, s0), s1 = fmaf(fmaxf(t1, -1e30f), e1, s1);
+  }
+  st.l += l0 + l1;
+  st.s += s0 + s1;
+}
+
+// The wave's n best so far: sorted keys, the n-th (0: fewer than n yet).
+struct Best {
+  u64 top, thr;
+};
+
+// Any chunk, NaN and -inf included: each lane offers its elements best first, all
+// lanes' next ones sorted and merged at a time, until none beats the n-th best.
+template <bool BF16>
+__device__ __forceinline__ void select_any(const Row& r, int w, int lane, int n,
+                                           const float (&z)[kPerLane], Best& b) {
   uint32_t key[kPerLane];
-  const bool full = w * kLogprobChunk >= off && (w + 1) * kLogprobChunk <= off + a.V;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    key[i] = order_of(z[i]);
-    const int e = e0 + (i / VE) * 64 * VE + i % VE;
-    if (!full && (e < off || e >= off + a.V)) key[i] = 0u;
+    const int e = place<BF16>(w, lane, i);
+    key[i] = e >= r.off && e < r.end ? order_of(z[i]) : 0u;
   }
-  // key64 of this lane's element i; elements outside the row rank last
-  auto whole = [&](uint32_t k, int i) -> u64 {
-    const int e = e0 + (i / VE) * 64 * VE + i % VE;
-    if (e < off || e >= off + a.V) return 0;
-    return (u64)k << 32 | (0xffffffffu - (uint32_t)(e - off));
-  };
-  uint32_t ck = 0;
-  int ci = kPerLane - 1;
-#pragma unroll
-  for (int i = kPerLane - 1; i >= 0; --i)
-    if (key[i] >= ck) ck = key[i], ci = i;
-  u64 cur = whole(ck, ci);
-  u64 top = wave_sort(cur, lane);
-  u64 thr = lane64(top, a.n_top - 1);
+  uint32_t ck = 0xffffffffu;  // the lane's last offer
+  int ci = kPerLane;
+  bool going = true;
   while (true) {
-    // this lane's next element after (ck, ci); none if the last fell short
     uint32_t nk = 1;  // 0: outside the row
     int ni = -1;
-    if (cur >= thr && cur != 0) {
+    if (going) {
 #pragma unroll
       for (int i = kPerLane - 1; i >= 0; --i)
         if ((key[i] < ck || (key[i] == ck && i > ci)) && key[i] >= nk) nk = key[i], ni = i;
     }
-    cur = ni >= 0 ? whole(nk, ni) : 0;
+    u64 cur = 0;
+    if (ni >= 0) cur = (u64)nk << 32 | (0xffffffffu - (uint32_t)(place<BF16>(w, lane, ni) - r.off));
+    if (cur <= b.thr) cur = 0;
+    going = cur != 0;
     ck = nk, ci = ni;
-    if (cur <= thr) cur = 0;
-    if (!__ballot(cur != 0)) break;
-    top = wave_merge(top, wave_sort(cur, lane), lane);
-    thr = lane64(top, a.n_top - 1);
+    if (!__ballot(going)) break;
+    b.top = wave_merge(b.top, wave_sort(cur, lane), lane);
+    b.thr = lane64(b.top, n - 1);
   }
-  // rank-major, so that the join sees every wave's best first
-  if (lane < a.n_top) a.pk[((size_t)t * a.n_top + lane) * a.W + w] = top;
 }
 
-// One block per row: joins the waves' sums and candidates.
+// Adds chunk w (its values z, their lane maximum) to the n best.  cand: this wave's
+// room for kCand keys in LDS.
+constexpr int kCand = 256;
 template <bool BF16>
-__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
-  const int t = blockIdx.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  __shared__ float sm[4], sl[4], ss[4];
-  __shared__ u64 st[4][64];
-  const size_t p0 = (size_t)t * a.W;
-  float M = -INFINITY;
-  for (int i = threadIdx.x; i < a.W; i += 256) M = fmaxf(M, a.pm[p0 + i]);
-  M = wave_max(M);
-  if (lane == 0) sm[wv] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float l = 0.0f, s = 0.0f;
-  for (int i = threadIdx.x; i < a.W; i += 256) {
-    const float m = a.pm[p0 + i], li = a.pl[p0 + i];
-    if (m == -INFINITY) {
-      l += li;  // 0, or NaN where the wave held nothing but NaN and -inf
-      continue;
+__device__ __forceinline__ void select_chunk(const Row& r, int w, int lane, int n, bool nan,
+                                             const float (&z)[kPerLane], float lane_max, Best& b,
+                                             u64* cand) {
+  constexpr int VE = BF16 ? 8 : 4;
+  const bool have = b.thr != 0;
+  // elements of a later chunk have higher ids: they must exceed the n-th best
+  const float least = have ? order_value((uint32_t)(b.thr >> 32)) : -INFINITY;
+  nan |= least != least;
+  if (!nan && have && !__ballot(lane_max > least)) return;
+  if (n == 1 && !nan) {
+    // the maximum and its first place
+    const float best = wave_max(lane_max);
+    if (best != -INFINITY) {
+      int at = kPerLane;
+#pragma unroll
+      for (int i = kPerLane - 1; i >= 0; --i)
+        if (z[i] == best) at = i;
+      const int id = wave_min_all(
+          at < kPerLane ? place<BF16>(w, lane, 0) + (at / VE) * 64 * VE + at % VE - r.off
+                        : 0x7fffffff);
+      b.thr = (u64)order_of(best) << 32 | (0xffffffffu - (uint32_t)id);
+      b.top = lane == 0 ? b.thr : 0;
+      return;
     }
-    const float d = m - M, e = __expf(d);
-    l = fmaf(e, li, l);
-    s = fmaf(e, fmaf(d, li, a.ps[p0 + i]), s);
   }
-  l = wave_sum_dpp(l);
-  s = wave_sum_dpp(s);
-  if (lane == 0) sl[wv] = l, ss[wv] = s;
-  u64 top = 0;
-  if (a.n_top) {
-    const int total = a.n_top * a.W;
-    const u64* pk = a.pk + (size_t)t * total;
-    u64 thr = 0;
-    for (int b = wv * 64; b < total; b += 256) {
-      u64 c = b + lane < total ? pk[b + lane] : 0;
-      if (c <= thr) c = 0;
-      if (!__ballot(c != 0)) continue;
-      top = wave_merge(top, wave_sort(c, lane), lane);
-      thr = lane64(top, a.n_top - 1);
+  float tau = least;
+  if (!nan && !have)
+    tau = order_value(__builtin_amdgcn_readlane(wave_sort(order_of(lane_max), lane), n - 1));
+  if (nan || tau == -INFINITY) {
+    select_any<BF16>(r, w, lane, n, z, b);
+    return;
+  }
+  uint32_t mask = 0;  // bit 31 - i: element i is a candidate
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) mask = 2 * mask + ((have ? z[i] > tau : z[i] >= tau) ? 1u : 0u);
+  const int count = (int)wave_sum_dpp((float)__popc(mask));
+  if (count > kCand) {  // ties in their hundreds
+    select_any<BF16>(r, w, lane, n, z, b);
+    return;
+  }
+  int at = 0;
+  while (true) {
+    const u64 some = __ballot(mask != 0);
+    if (!some) break;
+    if (mask) {
+      const int i = __clz(mask);
+      mask &= ~(0x80000000u >> i);
+      const int e = place<BF16>(w, lane, i);
+      const int p = at + __popcll(some & (((u64)1 << lane) - 1));
+      cand[p] = (u64)order_of(load_z<BF16>(r.base, e)) << 32 | (0xffffffffu - (uint32_t)(e - r.off));
     }
-    st[wv][lane] = top;
+    at += __popcll(some);
   }
+  __builtin_amdgcn_wave_barrier();
+  for (int i = 0; i < count; i += 64) {
+    u64 c = i + lane < count ? cand[i + lane] : 0;
+    if (c <= b.thr) c = 0;
+    if (!__ballot(c != 0)) continue;
+    b.top = wave_merge(b.top, wave_sort(c, lane), lane);
+    b.thr = lane64(b.top, n - 1);
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Stats and n best of the waves of a block, joined: wave 0 returns the row's (all lanes).
+// NW waves, `top` valid where n > 0.
+template <int NW>
+__device__ __forceinline__ void join_waves(Stats& st, u64& top, int n, int lane, int wv,
+                                           float* sm, u64 (*sk)[64]) {
+  st.l = wave_sum_dpp(st.l);
+  st.s = wave_sum_dpp(st.s);
+  if constexpr (NW == 1) return;
+  if (lane == 0) sm[wv] = st.m, sm[NW + wv] = st.l, sm[2 * NW + wv] = st.s;
+  if (n) sk[wv][lane] = top;
   __syncthreads();
+  if (n) {
+#pragma unroll
+    for (int half = NW / 2; half > 0; half >>= 1) {
+      if (wv < half) {
+        top = wave_merge(top, sk[wv + half][lane], lane);
+        sk[wv][lane] = top;
+      }
+      __syncthreads();
+    }
+  }
   if (wv) return;
-  l = sl[0] + sl[1] + sl[2] + sl[3];
-  s = ss[0] + ss[1] + ss[2] + ss[3];
-  const bool empty = M == -INFINITY && l == 0.0f;  // every logit is -inf
-  const float ll = logf(l);
+  float M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) M = fmaxf(M, sm[i]);
+  float l = 0.0f, s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) add_part(sm[i], sm[NW + i], sm[2 * NW + i], M, l, s);
+  st.m = M, st.l = l, st.s = s;
+}
+
+// The row's outputs from its joined statistics (one wave).
+template <bool BF16>
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int t, int lane, const Stats& st,
+                                          u64 top) {
+  const bool empty = st.m == -INFINITY && st.l == 0.0f;  // every logit is -inf
+  const float ll = logf(st.l);
   if (lane == 0) {
-    if (a.entropy) a.entropy[t] = empty ? 0.0f : ll - s / l;
+    if (a.entropy) a.entropy[t] = empty ? 0.0f : ll - st.s / st.l * kLn2;
     if (a.tokens) {
       const int tok = a.tokens[t];
       float lp = 0.0f;
       if (tok >= 0 && tok < a.V) {
         const float z = load_z<BF16>(
             (const uint8_t*)a.z + (size_t)t * a.row_stride * (BF16 ? 2 : 4), tok);
-        lp = empty ? -INFINITY : (z - M) - ll;
+        lp = empty ? -INFINITY : (z - st.m) - ll;
       } else if (tok >= a.V && a.status) {
         set_status(a.status, MOE_STATUS_BAD_TOKEN);
       }
       a.logprob[t] = lp;
     }
   }
-  if (a.n_top == 0) return;
-#pragma unroll
-  for (int k = 1; k < 4; ++k) top = wave_merge(top, st[k][lane], lane);
   if (lane < a.n_top) {
     const float z = order_value((uint32_t)(top >> 32));
     a.top_ids[(size_t)t * a.n_top + lane] = (int32_t)(0xffffffffu - (uint32_t)top);
-    a.top_logprobs[(size_t)t * a.n_top + lane] = empty ? -INFINITY : (z - M) - ll;
+    a.top_logprobs[(size_t)t * a.n_top + lane] = empty ? -INFINITY : (z - st.m) - ll;
   }
 }
 
-hipError_t launch_logprobs(const LogprobArgs& a, bool bf16, hipStream_t st) {
-  const dim3 grid(a.T, (a.W + 3) / 4);
-  if (bf16) {
-    logprob_chunk_kernel<true><<<grid, 256, 0, st>>>(a);
-    logprob_join_kernel<true><<<a.T, 256, 0, st>>>(a);
-  } else {
-    logprob_chunk_kernel<false><<<grid, 256, 0, st>>>(a);
-    logprob_join_kernel<false><<<a.T, 256, 0, st>>>(a);
+}  // namespace
+
+// grid (T, ceil(W / waves of a block)): a wave takes one chunk of one row.
+template <bool BF16>
+__global__ __launch_bounds__(256) void logprob_chunk_kernel(LogprobArgs a) {
+  __shared__ u64 cand[4][kCand];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int t = blockIdx.x, w = blockIdx.y * (blockDim.x >> 6) + wv;
+  if (w >= a.W) return;
+  const Row r = row_of<BF16>(a, t);
+  uint4 raw[kMaxWords];
+  float z[kPerLane];
+  load_chunk<BF16>(r, w, lane, raw);
+  unpack_chunk<BF16>(r, w, lane, raw, z);
+  const float lane_max = max_of(z);
+  Stats st = {-INFINITY, 0.0f, 0.0f};
+  add_chunk(z, lane_max, st);
+  const float l = wave_sum_dpp(st.l), s = wave_sum_dpp(st.s);
+  const size_t part = (size_t)t * a.W + w;
+  if (lane == 0) a.pm[part] = st.m, a.pl[part] = l, a.ps[part] = s;
+  if (a.n_top == 0) return;
+  Best b = {0, 0};
+  select_chunk<BF16>(r, w, lane, a.n_top, !(l < INFINITY), z, lane_max, b, cand[wv]);
+  // rank-major, so that the join sees every wave's best first
+  if (lane < a.n_top) a.pk[((size_t)t * a.n_top + lane) * a.W + w] = b.top;
+}
+
+// One block of NW waves per row: joins its chunks' sums and candidates.
+template <bool BF16, int NW>
+__global__ __launch_bounds__(64 * NW) void logprob_join_kernel(LogprobArgs a) {
+  __shared__ float sm[3 * NW];
+  __shared__ u64 sk[NW][64];
+  const int t = blockIdx.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const size_t p0 = (size_t)t * a.W;
+  Stats st = {-INFINITY, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < a.W; i += 64 * NW) st.m = fmaxf(st.m, a.pm[p0 + i]);
+  st.m = wave_max(st.m);
+  for (int i = threadIdx.x; i < a.W; i += 64 * NW)
+    add_part(a.pm[p0 + i], a.pl[p0 + i], a.ps[p0 + i], st.m, st.l, st.s);
+  Best b = {0, 0};
+  const int total = a.n_top * a.W;
+  const u64* pk = a.pk + (size_t)t * total;
+  if (a.n_top == 1) {
+    for (int i = threadIdx.x; i < total; i += 64 * NW) b.top = b.top > pk[i] ? b.top : pk[i];
+    b.top = wave_largest(b.top);
+    if (lane) b.top = 0;
+  } else if (a.n_top) {
+    for (int i = wv * 64; i < total; i += 64 * NW) {
+      u64 c = i + lane < total ? pk[i + lane] : 0;
+      if (c <= b.thr) c = 0;
+      if (!__ballot(c != 0)) continue;
+      b.top = wave_merge(b.top, wave_sort(c, lane), lane);
+      b.thr = lane64(b.top, a.n_top - 1);
+    }
   }
+  join_waves<NW>(st, b.top, a.n_top, lane, wv, sm, sk);
+  if (wv == 0) write_row<BF16>(a, t, lane, st, b.top);
+}
+
+// One block per row, its four waves walking the chunks.
+template <bool BF16>
+__global__ __launch_bounds__(256) void logprob_row_kernel(LogprobArgs a) {
+  __shared__ u64 cand[4][kCand];
+  __shared__ float sm[12];
+  __shared__ u64 sk[4][64];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int t = blockIdx.x;
+  const Row r = row_of<BF16>(a, t);
+  Stats st = {-INFINITY, 0.0f, 0.0f};
+  Best b = {0, 0};
+  uint4 raw[kMaxWords];
+  if (wv < a.W) load_chunk<BF16>(r, wv, lane, raw);
+  for (int w = wv; w < a.W; w += 4) {
+    float z[kPerLane];
+    unpack_chunk<BF16>(r, w, lane, raw, z);
+    if (w + 4 < a.W) load_chunk<BF16>(r, w + 4, lane, raw);
+    const float lane_max = max_of(z);
+    add_chunk(z, lane_max, st);
+    if (a.n_top)
+      select_chunk<BF16>(r, w, lane, a.n_top, __ballot(!(st.l < INFINITY)) != 0, z, lane_max, b,
+                         cand[wv]);
+  }
+  join_waves<4>(st, b.top, a.n_top, lane, wv, sm, sk);
+  if (wv == 0) write_row<BF16>(a, t, lane, st, b.top);
+}
+
+namespace {
+
+template <bool BF16>
+void launch_type(const LogprobArgs& a, hipStream_t st) {
+  if (a.by_row) {
+    logprob_row_kernel<BF16><<<a.T, 256, 0, st>>>(a);
+    return;
+  }
+  // a wave per block while that does not fill the chip: each then has a CU's loads
+  if ((int64_t)a.T * a.W <= 1024)
+    logprob_chunk_kernel<BF16><<<dim3(a.T, a.W), 64, 0, st>>>(a);
+  else
+    logprob_chunk_kernel<BF16><<<dim3(a.T, (a.W + 3) / 4), 256, 0, st>>>(a);
+  if (a.W * (a.n_top ? a.n_top : 1) <= 256)
+    logprob_join_kernel<BF16, 1><<<a.T, 64, 0, st>>>(a);
+  else
+    logprob_join_kernel<BF16, 16><<<a.T, 1024, 0, st>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_logprobs(const LogprobArgs& a, bool bf16, hipStream_t st) {
+  if (bf16)
+    launch_type<true>(a, st);
+  else
+    launch_type<false>(a, st);
   return hipGetLastError();
 }
 

@@ -123,8 +123,13 @@ size_t attn_bytes(const AttnArgs& a) {
          up256((size_t)(a.n_prefix_parts + a.n_own_parts) * a.n_tok * a.Hq * a.D * 4);
 }
 
+// rows from which a block walks each row (256 rows of 50021: 27 us so, 20 with a wave per
+// chunk and a join; 512 rows: 33 either way)
+constexpr int kLogprobRows = 512;
+
 struct LogprobLayout {
   int W;
+  bool by_row;
   size_t pm, pl, ps, pk, total;
 };
 
@@ -133,7 +138,10 @@ struct LogprobLayout {
 LogprobLayout logprob_layout(int T, int V, int n_top) {
   LogprobLayout L;
   L.W = ceil_div(V + 7, kLogprobChunk);
-  const size_t n = (size_t)T * L.W;
+  // two rows per CU keep a block per row busy; without partials nothing is needed, but
+  // a workspace has a size
+  L.by_row = T >= kLogprobRows;
+  const size_t n = L.by_row ? 1 : (size_t)T * L.W;
   L.pm = 0;
   L.pl = L.pm + up256(n * 4);
   L.ps = L.pl + up256(n * 4);
@@ -292,6 +300,7 @@ int token_logprobs(const void* z, int32_t z_dtype, int64_t row_stride, int32_t T
   LogprobArgs a;
   memset(&a, 0, sizeof a);
   a.z = z, a.row_stride = row_stride, a.T = T, a.V = V, a.W = L.W, a.n_top = n_top;
+  a.by_row = L.by_row;
   a.tokens = tokens, a.logprob = logprob, a.entropy = entropy;
   a.top_ids = top_ids, a.top_logprobs = top_logprobs, a.status = status;
   uint8_t* p = (uint8_t*)ws;

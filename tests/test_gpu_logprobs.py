@@ -76,6 +76,47 @@ def test_matches_64_bit_log_softmax(dt, n):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [0, 1, 7, 64])
+def test_many_rows(dt, n):
+    """Enough rows for the kernel that walks a row with one block: random rows, rows
+    of few values (ties), sorted ones both ways, masked ones."""
+    rng = np.random.default_rng(n)
+    T = 600
+    for V in (70, 2049, 9001, 20000):
+        print(dt, n, V, flush=True)
+        z = torch.from_numpy((3 * rng.standard_normal((T, V + 1))).astype(np.float32)).to(dt)
+        z[5] = torch.round(z[5])
+        z[6] = z[6].sort().values
+        z[7] = z[7].sort(descending=True).values
+        z[8, 40:] = -float("inf")
+        z[9] = 1.5
+        z[10, ::3] = -float("inf")
+        z[:, V:] = 1e30
+        tok = rng.integers(0, 40, T)
+        check(z, V, tok, min(n, 40), call(z, V, tok, min(n, 40)))
+        k = min(n, V)
+        check(z[:8], V, tok[:8], k, [a[:8] for a in call(z, V, tok, k)])
+
+
+def test_nan_rows_among_many():
+    T, V, n = 520, 6000, 5
+    z = torch.randn((T, V))
+    z[3, 100] = float("nan")
+    z[4, 5000] = float("inf")
+    z[5] = float("nan")
+    z[5, [70, 3000]] = torch.tensor([1.0, 2.0])
+    tok = np.full(T, 7)
+    lp, ent, ids, tlp = call(z, V, tok, n)
+    ok = [i for i in range(T) if i not in (3, 4, 5)]
+    check(z[ok], V, tok[ok], n, [a[ok] for a in (lp, ent, ids, tlp)])
+    x = np.where(np.isnan(z.numpy()), -np.inf, z.numpy())
+    for r in (3, 4):
+        assert np.isnan(lp[r]) and np.isnan(ent[r])
+        assert np.array_equal(ids[r], np.argsort(-x[r], kind="stable")[:n])
+    assert np.array_equal(ids[5], [3000, 70, 0, 1, 2])
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 def test_ties_go_to_the_lowest_id(dt):
     rng = np.random.default_rng(1)
     for V in (100, 2048, 5000, 20000):
