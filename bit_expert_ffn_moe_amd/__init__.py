@@ -133,10 +133,10 @@ EXPORTED = tuple(_sigs)
 
 
 def _ptr(a):
-    if a is None:
-        return None
-    if isinstance(a, int):
+    if a is None or type(a) is int:
         return a
+    if isinstance(a, int):
+        return int(a)
     return a.data_ptr()
 
 
