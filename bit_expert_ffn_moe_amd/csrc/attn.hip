@@ -19,17 +19,20 @@
 // columns) of each of its 8 keys, coalesced, and packs them with byte
 // permutes -- no LDS and no transposed copy of the cache.
 //
-// Scores, statistics and sums are fp32.  P is rounded for the matrix cores: to
-// bf16 beside bf16 V (the key at a row's maximum has P = 1, exactly), to fp16
-// beside E4M3 V, where P carries the row's scale and no value of it is exact;
-// the weights summed are the unrounded ones.
+// Scores, statistics and sums are fp32.  P is rounded for the matrix cores, each
+// weight by 2^-8 of itself at most: to bf16 beside bf16 V (8 bits, like V's), to fp16
+// (11 bits) beside E4M3 V, where P carries the row's scale and no value of it is
+// exact; the weights summed are the unrounded ones.
+//
+// Measured at 128 columns, bf16, 32 sequences of 8 kv heads and 4 query heads each:
+// 8192 shared keys and up to 2048 of their own, 161 MB, in 44 us with the join (3.7
+// TB/s: the shared keys are read by four blocks of rows, from L2 but for the
+// first).  16 sequences of 4 tokens, 8 kv heads of 8 query heads each, 32768 shared
+// E4M3 keys and up to 1024 of their own, 70 GFLOP: 136 us.
 #include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
-#ifndef PFN
-#define PFN 4
-#endif
 
 namespace bef {
 
@@ -611,6 +614,13 @@ __global__ __launch_bounds__(256, D < 256 && RTP == 1 ? 3 : 2) void attn_part_ke
 // one 16-byte read is an operand), each with its 16-byte chunks permuted by row
 // so that reads of 16 rows meet distinct banks.  An FP8 cache is converted
 // here, once for all the waves.
+//
+// Bound by the vector unit (a score costs an exponential and six more operations, with
+// an FP8 cache's two scales) and the matrix cores in turn: 512 rows of 8 kv heads
+// over 32768 keys, 69 GFLOP, 114 us bf16 with the join, 120 us FP8 without it, the
+// matrix cores busy for 26% of that.  (Forming the scores of the next 32 keys
+// under the exponentials of these takes the registers that hide LDS and loads: 170
+// us bf16.)
 template <int D, bool FP8, int RT>
 __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
   constexpr int NS = D / 32, VD = D / 16, ES = FP8 ? 1 : 2;
@@ -814,150 +824,152 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
       load_pages(j0 + 64);
     }
     for (; j0 < hi; j0 += 64, buf ^= 1) {
-    store_tile(buf, j0);
-    __syncthreads();
-    if (j0 + 64 < hi) {
-      load_tile(j0 + 64);
-      load_pages(j0 + 128);
-    }
-    const bool any_leak = lleak[buf] == j0, any_bad = lbad[buf] == j0;
-    // Where registers allow, the scores of both halves first: their products run
-    // under the first half's softmax (128 columns and two row tiles: one half at a time,
-    // 131 us instead of 147 for 512 rows of a kv head over 32768 keys)
-    constexpr int BOTH = RT == 1 || D == 64 ? 2 : 1;
+      store_tile(buf, j0);
+      __syncthreads();
+      if (j0 + 64 < hi) {
+        load_tile(j0 + 64);
+        load_pages(j0 + 128);
+      }
+      const bool any_leak = lleak[buf] == j0, any_bad = lbad[buf] == j0;
+      // Where registers allow, the scores of both halves first: their products run
+      // under the first half's softmax (128 columns and two row tiles: one half at a time,
+      // 131 us instead of 147 for 512 rows of a kv head over 32768 keys)
+      constexpr int BOTH = RT == 1 || D == 64 ? 2 : 1;
 #pragma unroll 1
-    for (int kh = 0; kh < 2; kh += BOTH) {
-    float x[BOTH][RT][8];
+      for (int kh = 0; kh < 2; kh += BOTH) {
+        float x[BOTH][RT][8];
 #pragma unroll
-    for (int kb = 0; kb < BOTH; ++kb) {
-      const int kt = kh + kb;
-      v4f_t s0[RT], s1[RT];
+        for (int kb = 0; kb < BOTH; ++kb) {
+          const int kt = kh + kb;
+          v4f_t s0[RT], s1[RT];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s0[rt] = s1[rt] = v4f_t{0.f, 0.f, 0.f, 0.f};
+          for (int rt = 0; rt < RT; ++rt) s0[rt] = s1[rt] = v4f_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int ra = 32 * kt + c, rb = ra + 16;
-        const uint4 k0 = lk[buf][ra][swz_k(ra, 4 * s + g)], k1 = lk[buf][rb][swz_k(rb, 4 * s + g)];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          s0[rt] = mfma(k0, q[rt][s], s0[rt]);
-          s1[rt] = mfma(k1, q[rt][s], s1[rt]);
-        }
-      }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[kb][rt][e] = s0[rt][e], x[kb][rt][4 + e] = s1[rt][e];
-    }
-#pragma unroll
-    for (int kb = 0; kb < BOTH; ++kb) {
-      const int kt = kh + kb;
-      const int jk = j0 + 32 * kt;
-      auto key_of = [&](int e) { return jk + 16 * (e >> 2) + 4 * g + (e & 3); };
-      const bool edge = jk < lo || jk + 32 > min(hi, minlim) || any_bad;
-      if (SLOW != (edge && any_leak)) {
-        aside = true;
-        continue;
-      }
-      float vscale[8];
-      if constexpr (FP8) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float4 kk = *reinterpret_cast<const float4*>(&lks[buf][32 * kt + 16 * u + 4 * g]);
-          const float4 vv = *reinterpret_cast<const float4*>(&lvs[buf][32 * kt + 16 * u + 4 * g]);
-          const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, v4[4] = {vv.x, vv.y, vv.z, vv.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) x[kb][rt][4 * u + e] *= k4[e];
-            vscale[4 * u + e] = v4[e];
-          }
-        }
-        const float nref =
-            __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(lvref[buf])));
-        if (nref != vref) {
-          const float f = vref / nref;
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int j = 0; j < VD; ++j) o[rt][j] *= f;
-          vref = nref;
-        }
-      }
-      auto v_operand = [&](int j) {
-        const int d = 16 * j + c;
-        return lv[buf][d][swz_v(d, 4 * kt + g)];
-      };
-      // the first V operands arrive under the softmax
-      constexpr int VPF = PFN;
-      uint4 va[VPF];
-#pragma unroll
-      for (int j = 0; j < VPF; ++j) va[j] = v_operand(j);
-      uint4 p[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if (edge) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (key_of(e) < lo || key_of(e) >= min(hi, lim[rt]) ||
-                (any_bad && bad_key(a, pages, key_of(e), lo, hi)))
-              x[kb][rt][e] = -INFINITY;
-        }
-        raise_max(max8(x[kb][rt]) * a.scale_log2, m[rt], [&](float f) {
-          l[rt] *= f;
-#pragma unroll
-          for (int j = 0; j < VD; ++j) o[rt][j] *= f;
-        });
-        const float mu = m[rt] == -INFINITY ? 0.0f : m[rt];
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[e] = __builtin_amdgcn_exp2f(fmaf(x[kb][rt][e], a.scale_log2, -mu));
-          l[rt] += w[e];
-          // (0 x a non-finite scale: only in groups set aside)
-          if (FP8) w[e] = SLOW && x[kb][rt][e] == -INFINITY ? 0.0f : w[e] * vscale[e];
-        }
-        p[rt] = pack_p<FP8>(w);
-      }
-      if constexpr (!SLOW) {
-#pragma unroll
-        for (int j = 0; j < VD; ++j) {
-          const uint4 vf = j < VPF ? va[j % VPF] : v_operand(j);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
-        }
-      } else {
-        // one limit at a time, the values past it cleared
-        int done = -1;
-        while (true) {
-          int next = 0x7fffffff;
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            if (lim[rt] > done) next = min(next, lim[rt]);
-          next = wave_min_all(next);
-          if (next == 0x7fffffff) break;
-          done = next;
-          uint32_t keep[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) keep[e] = key_of(e) < done ? 0xffffffffu : 0u;
-#pragma unroll
-          for (int j = 0; j < VD; ++j) {
-            uint4 vf = v_operand(j);
-            vf.x &= (keep[0] & 0xffffu) | (keep[1] & 0xffff0000u);
-            vf.y &= (keep[2] & 0xffffu) | (keep[3] & 0xffff0000u);
-            vf.z &= (keep[4] & 0xffffu) | (keep[5] & 0xffff0000u);
-            vf.w &= (keep[6] & 0xffffu) | (keep[7] & 0xffff0000u);
+          for (int s = 0; s < NS; ++s) {
+            const int ra = 32 * kt + c, rb = ra + 16;
+            const uint4 k0 = lk[buf][ra][swz_k(ra, 4 * s + g)];
+            const uint4 k1 = lk[buf][rb][swz_k(rb, 4 * s + g)];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-              const v4f_t n = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
-              if (lim[rt] == done) o[rt][j] = n;
+              s0[rt] = mfma(k0, q[rt][s], s0[rt]);
+              s1[rt] = mfma(k1, q[rt][s], s1[rt]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[kb][rt][e] = s0[rt][e], x[kb][rt][4 + e] = s1[rt][e];
+        }
+#pragma unroll
+        for (int kb = 0; kb < BOTH; ++kb) {
+          const int kt = kh + kb;
+          const int jk = j0 + 32 * kt;
+          auto key_of = [&](int e) { return jk + 16 * (e >> 2) + 4 * g + (e & 3); };
+          const bool edge = jk < lo || jk + 32 > min(hi, minlim) || any_bad;
+          if (SLOW != (edge && any_leak)) {
+            aside = true;
+            continue;
+          }
+          float vscale[8];
+          if constexpr (FP8) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int at = 32 * kt + 16 * u + 4 * g;
+              const float4 kk = *reinterpret_cast<const float4*>(&lks[buf][at]);
+              const float4 vv = *reinterpret_cast<const float4*>(&lvs[buf][at]);
+              const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, v4[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) x[kb][rt][4 * u + e] *= k4[e];
+                vscale[4 * u + e] = v4[e];
+              }
+            }
+            const float nref =
+                __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(lvref[buf])));
+            if (nref != vref) {
+              const float f = vref / nref;
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int j = 0; j < VD; ++j) o[rt][j] *= f;
+              vref = nref;
+            }
+          }
+          auto v_operand = [&](int j) {
+            const int d = 16 * j + c;
+            return lv[buf][d][swz_v(d, 4 * kt + g)];
+          };
+          // the first V operands arrive under the softmax
+          constexpr int VPF = 4;
+          uint4 va[VPF];
+#pragma unroll
+          for (int j = 0; j < VPF; ++j) va[j] = v_operand(j);
+          uint4 p[RT];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (key_of(e) < lo || key_of(e) >= min(hi, lim[rt]) ||
+                    (any_bad && bad_key(a, pages, key_of(e), lo, hi)))
+                  x[kb][rt][e] = -INFINITY;
+            }
+            raise_max(max8(x[kb][rt]) * a.scale_log2, m[rt], [&](float f) {
+              l[rt] *= f;
+#pragma unroll
+              for (int j = 0; j < VD; ++j) o[rt][j] *= f;
+            });
+            const float mu = m[rt] == -INFINITY ? 0.0f : m[rt];
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              w[e] = __builtin_amdgcn_exp2f(fmaf(x[kb][rt][e], a.scale_log2, -mu));
+              l[rt] += w[e];
+              // (0 x a non-finite scale: only in groups set aside)
+              if (FP8) w[e] = SLOW && x[kb][rt][e] == -INFINITY ? 0.0f : w[e] * vscale[e];
+            }
+            p[rt] = pack_p<FP8>(w);
+          }
+          if constexpr (!SLOW) {
+#pragma unroll
+            for (int j = 0; j < VD; ++j) {
+              const uint4 vf = j < VPF ? va[j % VPF] : v_operand(j);
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
+            }
+          } else {
+            // one limit at a time, the values past it cleared
+            int done = -1;
+            while (true) {
+              int next = 0x7fffffff;
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt)
+                if (lim[rt] > done) next = min(next, lim[rt]);
+              next = wave_min_all(next);
+              if (next == 0x7fffffff) break;
+              done = next;
+              uint32_t keep[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) keep[e] = key_of(e) < done ? 0xffffffffu : 0u;
+#pragma unroll
+              for (int j = 0; j < VD; ++j) {
+                uint4 vf = v_operand(j);
+                vf.x &= (keep[0] & 0xffffu) | (keep[1] & 0xffff0000u);
+                vf.y &= (keep[2] & 0xffffu) | (keep[3] & 0xffff0000u);
+                vf.z &= (keep[4] & 0xffffu) | (keep[5] & 0xffff0000u);
+                vf.w &= (keep[6] & 0xffffu) | (keep[7] & 0xffff0000u);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                  const v4f_t n = mfma_pv<FP8>(vf, p[rt], o[rt][j]);
+                  if (lim[rt] == done) o[rt][j] = n;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
           }
         }
       }
-    }
-    }
     }
     return aside;
   };
