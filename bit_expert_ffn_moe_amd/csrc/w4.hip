@@ -15,8 +15,10 @@
 // scale group in both formats.
 //
 // Bound by the weights' bytes where there are many: 131072 x 4096 FP4, 285 MB, in
-// 47 us for one token and 69 us for 32 tokens (4.2 TB/s).  Small products are bound
+// 47 us for one token and 66 us for 32 tokens (4.3 TB/s).  Small products are bound
 // by latency: 4096 x 4096 FP4, one token, 3.9 us, where reading 9 MB takes 3.4.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -218,7 +220,10 @@ constexpr int kW4PassTiles = 16;  // tiles whose sums are kept over the passes
 // WHOLE: K is a multiple of 128, so every step is whole (one lane offset for all
 // weight loads; FP4: a step's four scale bytes are one aligned dword);
 // otherwise chunks are clamped into the row one by one.
-template <bool INT4, int S, int TT, int NG, int DEPTH, bool WHOLE>
+// MANY: a block has 2 DEPTH tiles or more, see the loop over them (as a variant of its
+// own, because its code makes short calls longer: 4096 x 4096 FP4, 4 tokens, 6.2 us
+// without it, 6.4 with; 32768 rows, 32 tokens, 26.4 us without it, 25.1 with).
+template <bool INT4, int S, int TT, int NG, int DEPTH, bool WHOLE, bool MANY>
 __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4Args a) {
   constexpr int NW = kW4Waves;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -227,7 +232,11 @@ __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4
   const int nch = a.K >> 5, nq = (nch + 3) >> 2;
   const int passes = (nq + NW * S - 1) / (NW * S);
   const int tiles = (a.N + 15) >> 4;
-  const int mine = ((int)blockIdx.x < tiles) ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  // neighbouring tiles on one XCD (blocks are dealt out over the eight in turn): a
+  // line of y, four tiles of a token, is put together in one L2 (131072 rows, FP4, 8
+  // tokens: 52.2 us, 54.5 with tiles in block order)
+  const int first = gridDim.x == 256 ? (blockIdx.x & 7) * 32 + (blockIdx.x >> 3) : blockIdx.x;
+  const int mine = first < tiles ? (tiles - first + gridDim.x - 1) / gridDim.x : 0;
   __shared__ float red[2][NW][TT * 4][64];
   __shared__ float keep[kW4PassTiles][TT * 256];
   __shared__ v4f_t xsum[INT4 ? NW : 1][S][NG][4 * TT];
@@ -236,16 +245,22 @@ __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4
   constexpr int NE = INT4 ? S * NG : S;                   // entries of a pass
   constexpr int NR = INT4 || WHOLE ? (NE + 3) / 4 : S;    // words per lane
   constexpr int NWO = WHOLE ? 1 : S;
+  // (without zero points, bytes of the scales are loaded in their place, from lines
+  // that are fetched anyway: no load is conditional)
+  const uint8_t* zero = a.zero ? a.zero : reinterpret_cast<const uint8_t*>(a.scale);
+  const int zsh = a.zero ? 0 : 1;
   struct Tile {
     u4_t w[S];
-    uint32_t sc[NR], zp[INT4 ? NR : 1];
+    // (as loaded: widened at once, they would be waited for at once)
+    std::conditional_t<INT4, uint16_t, uint32_t> sc[NR];
+    uint8_t zp[INT4 ? NR : 1];
   };
   // first row of this block's tile `it`: the last tile of the matrix ends at its
   // last row (rows it shares with the one before are computed twice, alike);
   // fewer than 16 rows: lanes past the last repeat it
   const int cr = min(c, a.N - 1);
   auto first_row = [&](int it) {
-    return max(0, min((int)(blockIdx.x + it * gridDim.x) * 16, a.N - 16));
+    return max(0, min((int)(first + it * gridDim.x) * 16, a.N - 16));
   };
   const int group_tiles = passes == 1 ? mine : kW4PassTiles;
   int buf = 0;
@@ -297,7 +312,7 @@ __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4
           if constexpr (INT4) {
             const uint8_t* sb = reinterpret_cast<const uint8_t*>(a.scale) + n0 * a.n_groups * 2;
             t.sc[r] = *reinterpret_cast<const uint16_t*>(sb + 2 * os[r]);
-            t.zp[r] = a.zero ? (a.zero + n0 * a.n_groups)[os[r]] : 8u;
+            t.zp[r] = (zero + (n0 * a.n_groups << zsh))[os[r] << zsh];
           } else if constexpr (WHOLE) {
             const uint8_t* sb = reinterpret_cast<const uint8_t*>(a.scale) + n0 * nch;
             t.sc[r] = *reinterpret_cast<const uint32_t*>(sb + os[r]);
@@ -377,99 +392,114 @@ __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4
       };
       int pending = -1;  // tile whose partial sums wait in LDS
       float rv[NTE][NW];
-      for (int itd = 0; itd < n_it; itd += DEPTH) {
+      auto step = [&](auto more, int it, Tile& cur) {
+        constexpr bool MORE = decltype(more)::value;
+        // the last tile's partial sums arrive while this one multiplies
+        if (pending >= 0) read_partials(rv);
+        // an offset the compiler cannot see through, or it keeps all the sums
+        // of x in registers over the tiles (and spills)
+        int xo = g;
+        asm volatile("" : "+v"(xo));
+        // FP4: the pass's scales, in every lane group
+        float gs[INT4 ? 4 : S < 4 ? 4 : S], gz[4];
+        if constexpr (!INT4 && WHOLE) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          const int it = itd + d;
-          if (it >= n_it) break;
-          Tile& cur = ring[d];
-          // the last tile's partial sums arrive while this one multiplies
-          if (pending >= 0) read_partials(rv);
-          // an offset the compiler cannot see through, or it keeps all the sums
-          // of x in registers over the tiles (and spills)
-          int xo = g;
-          asm volatile("" : "+v"(xo));
-          // FP4: the pass's scales, in every lane group
-          float gs[INT4 ? 4 : S < 4 ? 4 : S], gz[4];
-          if constexpr (!INT4 && WHOLE) {
+          for (int r = 0; r < NR; ++r)
+            spread<(NE < 4 ? NE : 4)>(__uint_as_float(cur.sc[r]), &gs[4 * r]);
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-              spread<(NE < 4 ? NE : 4)>(__uint_as_float(cur.sc[r]), &gs[4 * r]);
+          for (int i = 0; i < S; ++i)
+            gs[i] = ue8m0_operand((__float_as_uint(gs[i]) >> (8 * g)) & 255u);
+        } else if constexpr (!INT4) {
 #pragma unroll
-            for (int i = 0; i < S; ++i)
-              gs[i] = ue8m0_operand((__float_as_uint(gs[i]) >> (8 * g)) & 255u);
-          } else if constexpr (!INT4) {
+          for (int i = 0; i < S; ++i) gs[i] = ue8m0_operand(cur.sc[i]);
+        }
+        v4f_t acc[TT];
 #pragma unroll
-            for (int i = 0; i < S; ++i) gs[i] = ue8m0_operand(cur.sc[i]);
-          }
-          v4f_t acc[TT];
+        for (int t = 0; t < TT; ++t) acc[t] = v4f_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t = 0; t < TT; ++t) acc[t] = v4f_t{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < S; ++i) {
+          if constexpr (!INT4) {
 #pragma unroll
-          for (int i = 0; i < S; ++i) {
-            if constexpr (!INT4) {
+            for (int j = 0; j < 4; ++j) {
+              uint32_t pr[4];
+              codes8<false>(cur.w[i][j], gs[i], pr);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int t = 0; t < TT; ++t)
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf8_t, x[i][j][t]), __builtin_bit_cast(bf8_t, pr), acc[t],
+                    0, 0, 0);
+            }
+          } else {
+            // steps in order: without this their operands are formed at once and
+            // spill
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int per = 4 / NG;  // steps per word
+            if (i % per == 0) {
+              const float sc = bf16_to_f32(cur.sc[i / per]);
+              spread<(NE < 4 ? NE : 4)>(sc, gs);
+              const float z = a.zero ? (float)cur.zp[i / per] : 8.0f;
+              spread<(NE < 4 ? NE : 4)>(sc * z, gz);  // exact: 8 x 8 bits
+            }
+            uint32_t w[4] = {cur.w[i][0], cur.w[i][1], cur.w[i][2], cur.w[i][3]};
+            transpose4(w);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+              v4f_t dd[TT];
+#pragma unroll
+              for (int t = 0; t < TT; ++t) dd[t] = v4f_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = n * 4 / NG; j < (n + 1) * 4 / NG; ++j) {
                 uint32_t pr[4];
-                codes8<false>(cur.w[i][j], gs[i], pr);
+                codes8<true>(w[j], 1.0f, pr);
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
-                  acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                      __builtin_bit_cast(bf8_t, x[i][j][t]), __builtin_bit_cast(bf8_t, pr), acc[t],
+                  dd[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                      __builtin_bit_cast(bf8_t, x[i][j][t]), __builtin_bit_cast(bf8_t, pr), dd[t],
                       0, 0, 0);
               }
-            } else {
-              // steps in order: without this their operands are formed at once and
-              // spill
-              __builtin_amdgcn_sched_barrier(0);
-              constexpr int per = 4 / NG;  // steps per word
-              if (i % per == 0) {
-                const float sc = bf16_to_f32(cur.sc[i / per]);
-                spread<(NE < 4 ? NE : 4)>(sc, gs);
-                spread<(NE < 4 ? NE : 4)>(sc * (float)cur.zp[i / per], gz);  // exact: 8 x 8 bits
-              }
-              uint32_t w[4] = {cur.w[i][0], cur.w[i][1], cur.w[i][2], cur.w[i][3]};
-              transpose4(w);
 #pragma unroll
-              for (int n = 0; n < NG; ++n) {
-                v4f_t dd[TT];
+              for (int t = 0; t < TT; ++t) {
+                const v4f_t xs = xsum[wv][i][n][4 * t + xo];
 #pragma unroll
-                for (int t = 0; t < TT; ++t) dd[t] = v4f_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = n * 4 / NG; j < (n + 1) * 4 / NG; ++j) {
-                  uint32_t pr[4];
-                  codes8<true>(w[j], 1.0f, pr);
-#pragma unroll
-                  for (int t = 0; t < TT; ++t)
-                    dd[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf8_t, x[i][j][t]), __builtin_bit_cast(bf8_t, pr), dd[t],
-                        0, 0, 0);
-                }
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                  const v4f_t xs = xsum[wv][i][n][4 * t + xo];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    acc[t][e] = fmaf(gs[(NG * i + n) % 4], dd[t][e],
-                                     fmaf(-gz[(NG * i + n) % 4], xs[e], acc[t][e]));
-                  // (here, not sunk to the end with every dd and xs kept)
-                  asm volatile("" : "+v"(acc[t]));
-                }
+                for (int e = 0; e < 4; ++e)
+                  acc[t][e] = fmaf(gs[(NG * i + n) % 4], dd[t][e],
+                                   fmaf(-gz[(NG * i + n) % 4], xs[e], acc[t][e]));
+                // (here, not sunk to the end with every dd and xs kept)
+                asm volatile("" : "+v"(acc[t]));
               }
             }
           }
-          if (it + DEPTH < n_it) load_tile(it + DEPTH, cur);
-          if (pending >= 0) join(pending, rv);
-#pragma unroll
-          for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) red[buf][wv][4 * t + e][lane] = acc[t][e];
-          lds_barrier();
-          pending = it;
-          // the other half is written next: its readers are past this barrier
-          buf ^= 1;
         }
+        if (MORE || it + DEPTH < n_it) load_tile(it + DEPTH, cur);
+        if (pending >= 0) join(pending, rv);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) red[buf][wv][4 * t + e][lane] = acc[t][e];
+        lds_barrier();
+        pending = it;
+        // the other half is written next: its readers are past this barrier
+        buf ^= 1;
+      };
+      int itd = 0;
+      // While every tile has a successor to load, no load is conditional, so the waits
+      // leave the younger tiles' loads in flight (131072 rows, INT4, 16 tokens: 59.6 us;
+      // with conditional loads each tile waits for all: 70.4).  What came before, the
+      // activations, is waited for here, or it would be at every tile.
+      if (MANY && 2 * DEPTH <= n_it) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        do {
+#pragma unroll
+          for (int d = 0; d < DEPTH; ++d) step(std::true_type{}, itd + d, ring[d]);
+          itd += DEPTH;
+        } while (itd + 2 * DEPTH <= n_it);
       }
+      for (; itd < n_it; itd += DEPTH)
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+          if (itd + d >= n_it) break;
+          step(std::false_type{}, itd + d, ring[d]);
+        }
       if (pending >= 0) {
         read_partials(rv);
         join(pending, rv);
@@ -485,10 +515,15 @@ void launch_tiles(const W4Args& a, hipStream_t st) {
   // one block per CU walks its tiles: its waves hold the activations once
   const int tiles = (a.N + 15) / 16;
   const dim3 grid(tiles < 256 ? tiles : 256, (a.T + 16 * TT - 1) / (16 * TT));
-  if (a.K % 128 == 0)
-    w4_mfma_kernel<INT4, S, TT, NG, DEPTH, true><<<grid, 64 * kW4Waves, 0, st>>>(a);
+  const bool whole = a.K % 128 == 0, many = tiles >= 2 * DEPTH * 256;
+  if (whole && many)
+    w4_mfma_kernel<INT4, S, TT, NG, DEPTH, true, true><<<grid, 64 * kW4Waves, 0, st>>>(a);
+  else if (whole)
+    w4_mfma_kernel<INT4, S, TT, NG, DEPTH, true, false><<<grid, 64 * kW4Waves, 0, st>>>(a);
+  else if (many)
+    w4_mfma_kernel<INT4, S, TT, NG, DEPTH, false, true><<<grid, 64 * kW4Waves, 0, st>>>(a);
   else
-    w4_mfma_kernel<INT4, S, TT, NG, DEPTH, false><<<grid, 64 * kW4Waves, 0, st>>>(a);
+    w4_mfma_kernel<INT4, S, TT, NG, DEPTH, false, false><<<grid, 64 * kW4Waves, 0, st>>>(a);
 }
 
 template <bool INT4, int TT, int NG>
@@ -509,7 +544,7 @@ void launch_groups(const W4Args& a, hipStream_t st) {
   // One token on the vector unit: 2 rows a wave, 4 from 16384 rows on, where
   // there are waves enough (131072 x 4096 FP4: 50.0 us with 2, 47.1 with 4;
   // 4096 x 4096: 4.15 with 2, 4.73 with 4).  Two tokens too while rows are few
-  // (4096 x 4096 FP4: 5.1 us, 5.7 on the matrix cores; 131072 rows: 60.3 and 49.8).
+  // (4096 x 4096 FP4: 5.1 us, 5.7 on the matrix cores; 131072 rows: 60.3 and 48.4).
   if (a.T == 1 && a.N >= 16384) {
     w4_gemv_kernel<INT4, 1, 4><<<(a.N + 15) / 16, 256, 0, st>>>(a);
   } else if (a.T == 1) {
