@@ -235,7 +235,8 @@ __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4
   // neighbouring tiles on one XCD (blocks are dealt out over the eight in turn): a
   // line of y, four tiles of a token, is put together in one L2 (131072 rows, FP4, 8
   // tokens: 52.2 us, 54.5 with tiles in block order)
-  const int first = gridDim.x == 256 ? (blockIdx.x & 7) * 32 + (blockIdx.x >> 3) : blockIdx.x;
+  const int first =
+      gridDim.x % 8 ? blockIdx.x : (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   const int mine = first < tiles ? (tiles - first + gridDim.x - 1) / gridDim.x : 0;
   __shared__ float red[2][NW][TT * 4][64];
   __shared__ float keep[kW4PassTiles][TT * 256];
@@ -512,9 +513,14 @@ namespace {
 
 template <bool INT4, int S, int TT, int NG, int DEPTH>
 void launch_tiles(const W4Args& a, hipStream_t st) {
-  // one block per CU walks its tiles: its waves hold the activations once
-  const int tiles = (a.N + 15) / 16;
-  const dim3 grid(tiles < 256 ? tiles : 256, (a.T + 16 * TT - 1) / (16 * TT));
+  // One block per CU walks its tiles: its waves hold the activations once.  With few
+  // tiles a block, as many blocks as share them evenly: fewer read the activations (6144
+  // rows, FP4, 64 tokens: 23.3 us with 192 blocks of two tiles, 25.1 with 256), unless
+  // too few CUs would be left (4352 rows of 2048, 4 tokens: 5.5 us with 136, 5.3 with 256).
+  const int tiles = (a.N + 15) / 16, rounds = (tiles + 255) / 256;
+  const int even = (tiles + rounds - 1) / rounds;
+  const dim3 grid(tiles <= 256 ? tiles : even >= 160 ? even : 256,
+                  (a.T + 16 * TT - 1) / (16 * TT));
   const bool whole = a.K % 128 == 0, many = tiles >= 2 * DEPTH * 256;
   if (whole && many)
     w4_mfma_kernel<INT4, S, TT, NG, DEPTH, true, true><<<grid, 64 * kW4Waves, 0, st>>>(a);
