@@ -997,11 +997,13 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
 }
 
 // Joins a row's parts, weighted by 2^(m - M), and normalises.  D/4 lanes hold a
-// row's columns; 4 such groups a row take its parts in turn, 8 loads at a time.
+// row's columns; 4 such groups a row take its parts in turn, U loads at a time: 4
+// where that takes all in one round (16 parts), 8 beyond (4 sequences of 560 keys, the
+// whole call: 8.8 us, 9.1 with 8; one of 8192 keys: 11.0, 11.5 with 4).
 constexpr int kJoinGroups = 4;
-template <int D>
+template <int D, int U>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  constexpr int LPR = D / 4, RPB = 256 / (LPR * kJoinGroups), U = 8;
+  constexpr int LPR = D / 4, RPB = 256 / (LPR * kJoinGroups);
   __shared__ float4 so[RPB][kJoinGroups][LPR];
   __shared__ float2 sml[RPB][kJoinGroups];
   const int ln = threadIdx.x % LPR, pg = threadIdx.x / LPR % kJoinGroups,
@@ -1100,7 +1102,11 @@ void launch_all(const AttnArgs& a, hipStream_t st) {
     launch_dim<D, false>(a, st);
   constexpr int RPB = 256 / (D / 4 * kJoinGroups);
   const int64_t rows = (int64_t)a.n_tok * a.Hq;
-  attn_join_kernel<D><<<(unsigned)((rows + RPB - 1) / RPB), 256, 0, st>>>(a);
+  const unsigned blocks = (unsigned)((rows + RPB - 1) / RPB);
+  if (a.n_prefix_parts + a.n_own_parts <= 4 * kJoinGroups)
+    attn_join_kernel<D, 4><<<blocks, 256, 0, st>>>(a);
+  else
+    attn_join_kernel<D, 8><<<blocks, 256, 0, st>>>(a);
 }
 
 }  // namespace
