@@ -13,9 +13,9 @@
 // its n best so far (later elements then mostly fall short of its n-th best), and
 // joins them itself: bound by HBM and, closely, by the vector unit (an
 // exponential and ten more operations an element).
-// Measured: one row of 131072 fp32 with its 20 best 12.7 us, 32 rows of bf16 with 5
-// 14.7 us (two launches and their latencies); 4096 rows of 50021 bf16, 410 MB, 96 us
-// (4.3 TB/s).
+// Measured: one row of 131072 fp32 with its 20 best 12.8 us, 32 rows of bf16 with 5
+// 14.8 us (two launches and their latencies); 4096 rows of 50021 bf16, 410 MB, 86 us
+// (4.8 TB/s).
 //
 // A candidate is one 64-bit key: the logit's order in the high word (a
 // monotone map of fp32 to unsigned, NaN 1 and below every number, 0 for places
@@ -115,6 +115,12 @@ __device__ __forceinline__ u64 wave_merge(u64 a, u64 b, int lane) {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// (a - b) log2 e, not below -1e30: sums may be multiplied by it where their weight 2^it
+// is 0 (a and b of the type's lowest and highest values are 2^129 apart).
+__device__ __forceinline__ float log2_ratio(float a, float b) {
+  return fmaxf((a - b) * kLog2e, -1e30f);
+}
+
 __device__ __forceinline__ float max_of(const float (&z)[kPerLane]) {
   float m = z[0];
 #pragma unroll
@@ -129,7 +135,7 @@ __device__ __forceinline__ void add_part(float m, float li, float si, float M, f
     l += li;  // 0, or NaN where the part held nothing but NaN and -inf
     return;
   }
-  const float d = (m - M) * kLog2e, f = __builtin_amdgcn_exp2f(d);
+  const float d = log2_ratio(m, M), f = __builtin_amdgcn_exp2f(d);
   l = fmaf(f, li, l);
   s = fmaf(f, fmaf(d, li, si), s);
 }
@@ -215,28 +221,46 @@ __device__ __forceinline__ void unpack_chunk(const Row& r, int w, int lane,
 struct Stats {
   float m, l, s;
 };
+// l and s of a chunk, t_of giving each element's t (two sums each: shorter chains).
+template <class F>
+__device__ __forceinline__ void chunk_sums(const float (&z)[kPerLane], F&& t_of, float& l,
+                                           float& s) {
+  float l0 = 0.0f, l1 = 0.0f, s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPerLane; i += 2) {
+    const float t0 = t_of(z[i]), t1 = t_of(z[i + 1]);
+    const float e0 = __builtin_amdgcn_exp2f(t0), e1 = __builtin_amdgcn_exp2f(t1);
+    l0 += e0, l1 += e1;
+    s0 = fmaf(fmaxf(t0, -1e30f), e0, s0), s1 = fmaf(fmaxf(t1, -1e30f), e1, s1);
+  }
+  l = l0 + l1, s = s0 + s1;
+}
 __device__ __forceinline__ void add_chunk(const float (&z)[kPerLane], float lane_max, Stats& st) {
   const float m = fmaxf(st.m, wave_max(lane_max));
   if (m > st.m) {
     if (st.m != -INFINITY) {
-      const float d = (st.m - m) * kLog2e, f = __builtin_amdgcn_exp2f(d);
+      const float d = log2_ratio(st.m, m), f = __builtin_amdgcn_exp2f(d);
       st.s = f * fmaf(d, st.l, st.s);
       st.l *= f;
     }
     st.m = m;
   }
-  const float c = st.m == -INFINITY ? 0.0f : -st.m * kLog2e;
-  // two sums each: shorter chains
-  float l0 = 0.0f, l1 = 0.0f, s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPerLane; i += 2) {
-    const float t0 = fmaf(z[i], kLog2e, c), t1 = fmaf(z[i + 1], kLog2e, c);
-    const float e0 = __builtin_amdgcn_exp2f(t0), e1 = __builtin_amdgcn_exp2f(t1);
-    l0 += e0, l1 += e1;
-    s0 = fmaf(fmaxf(t0, -1e30f), e0, s0), s1 = fmaf(fmaxf(t1, -1e30f), e1, s1);
+  float l, s;
+  if (fabsf(m) <= 65536.0f) {
+    // One operation an element: t + d = z log2 e + c with c = -m log2 e rounded, so every
+    // term carries 2^d, d the rounding error of c (2^-8 at most here), which is taken
+    // out of the chunk's sums.
+    const float c = -m * kLog2e, d = fmaf(m, kLog2e, c), g = __builtin_amdgcn_exp2f(-d);
+    chunk_sums(z, [&](float v) { return fmaf(v, kLog2e, c); }, l, s);
+    st.l = fmaf(g, l, st.l);
+    st.s = fmaf(g, fmaf(-d, l, s), st.s);
+  } else {
+    // m log2 e may overflow and d be anything: subtracted first
+    const float r = m == -INFINITY ? 0.0f : m;
+    chunk_sums(z, [&](float v) { return (v - r) * kLog2e; }, l, s);
+    st.l += l;
+    st.s += s;
   }
-  st.l += l0 + l1;
-  st.s += s0 + s1;
 }
 
 // The wave's n best so far: sorted keys, the n-th (0: fewer than n yet).
@@ -381,9 +405,10 @@ template <bool BF16>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int t, int lane, const Stats& st,
                                           u64 top) {
   const bool empty = st.m == -INFINITY && st.l == 0.0f;  // every logit is -inf
-  const float ll = logf(st.l);
+  // the largest term is 1, whatever the sum's rounding: no log probability above 0
+  const float l = st.l < 1.0f ? 1.0f : st.l, ll = logf(l);
   if (lane == 0) {
-    if (a.entropy) a.entropy[t] = empty ? 0.0f : ll - st.s / st.l * kLn2;
+    if (a.entropy) a.entropy[t] = empty ? 0.0f : ll - st.s / l * kLn2;
     if (a.tokens) {
       const int tok = a.tokens[t];
       float lp = 0.0f;
