@@ -19,10 +19,13 @@
 // columns) of each of its 8 keys, coalesced, and packs them with byte
 // permutes -- no LDS and no transposed copy of the cache.
 //
-// Scores, statistics and sums are fp32.  P is rounded for the matrix cores, each
-// weight by 2^-8 of itself at most: to bf16 beside bf16 V (8 bits, like V's), to fp16
-// (11 bits) beside E4M3 V, where P carries the row's scale and no value of it is
-// exact; the weights summed are the unrounded ones.
+// Scores, statistics and sums are fp32.  P is rounded for the matrix cores: to bf16 beside
+// bf16 V, each weight by 2^-8 of itself at most; the weights summed are the unrounded ones.
+// Beside E4M3 V a weight is P times the key's V scale, no value of which is exact, and is
+// rounded to fp16: by 2^-11 of itself, or by 2^-29 of the row's largest weight where
+// that is more.  fp16 holds 2^40 in all, so a row's weights are formed against its own
+// largest P v_scale (raise_max's reference): a scale far from the others', of a key that the
+// row does not see or gives no weight, takes nothing from the weights beside it.
 //
 // Measured at 128 columns, bf16, 32 sequences of 8 kv heads and 4 query heads each:
 // 8192 shared keys and up to 2048 of their own, 161 MB, in 44 us with the join (3.7
@@ -131,28 +134,52 @@ __device__ __forceinline__ int row_limit(const AttnArgs& a, int t) {
   return p < 0 ? 0 : min(p + 1, a.max_keys);
 }
 
-// Raises the power of two `vref` to bound the lanes' scales vm (2^-100 at
-// least); `rescale` takes the sums over to it.
-template <class F>
-__device__ __forceinline__ void raise_vref(float vm, float& vref, F&& rescale) {
-  vm = __uint_as_float(__float_as_uint(quad_max(vm)) & 0x7f800000u);
-  vm = fmaxf(vm + vm, 0x1p-100f);
-  if (__ballot(vm > vref)) {
-    rescale(vref / vm);
-    vref = vm;
-  }
+// V scales of an E4M3 cache are multiplied in units of 2^-12 `bound`, a power of two taken
+// once, 4 to 8 times the first scales' largest.
+__device__ __forceinline__ float scale_bound(float first) {
+  const float b = 8.0f * __uint_as_float(__float_as_uint(first) & 0x7f800000u);
+  return __builtin_amdgcn_fmed3f(b, 0x1p-40f, 0x1p40f);
+}
+// Finite scales stay finite (times a weight of 0 they must be 0).
+__device__ __forceinline__ float scale_units(float v, float per) {
+  const float u = v * per;
+  return fabsf(v) < INFINITY ? __builtin_amdgcn_fmed3f(u, -0x1.fffffep127f, 0x1.fffffep127f) : u;
+}
+// log2 of a scale in those units against bound, within what leaves the sum of
+// 2^(score - reference) in fp32's range: scales of 2^-90 to 2^115 times bound.
+__device__ __forceinline__ float scale_log2_of(float u) {
+  return __builtin_amdgcn_fmed3f(__builtin_amdgcn_logf(fabsf(u)) - 12.0f, -90.0f, 115.0f);
+}
+// Scales near enough to bound that a weight may be bounded by P alone.
+__device__ __forceinline__ bool scale_far(float lo, float hi, float bound) {
+  return !(hi <= bound && lo >= bound * 0x1p-8f);
+}
+// Brings l to [1, 2) and m along, by the power of two 2^-k (exactly: k is whole).  References
+// that follow V scales say nothing of a part's weight; joined parts have to compare.
+__device__ __forceinline__ int unit_weight(float& m, float& l) {
+  const int e = (int)(__float_as_uint(l) >> 23) - 127;
+  const int k = l > 0.0f && l < INFINITY ? e : 0;
+  l = __builtin_amdgcn_ldexpf(l, -k);
+  m += (float)k;
+  return k;
 }
 
 __device__ __forceinline__ float max8(const float (&x)[8]) {
   return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
                fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 }
+__device__ __forceinline__ float min8(const float (&x)[8]) {
+  return fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])),
+               fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+}
 
 // The running maximum m of a lane column (log2 units), given this tile's largest
 // scores: P = 2^(score - m).  m is raised where a score passes it by more than
 // 3, so P is at most 8 and the sums are rescaled a few times, not at every
 // tile that holds a new maximum (most of the first dozens); a key that stands
-// out by more than that has P = 1 exactly.
+// out by more than that has P = 1 exactly.  With an E4M3 cache m is the reference of the
+// weights P v_scale: mx then is the largest score plus the log2 of its key's scale (or a
+// bound of it), and P = 2^(score - m) may be far from 1.
 template <class F>
 __device__ __forceinline__ void raise_max(float mx, float& m, F&& rescale) {
   if (__ballot(mx > m + 3.0f)) {
@@ -223,7 +250,8 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
 #pragma unroll
     for (int j = 0; j < VD; ++j) o[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
   }
-  float vref = 0.0f;  // FP8: o is in units of this power of two
+  // FP8: o is in units of 2^-12 bound (0: not yet known), of which a scale of 1 is `per`
+  float bound = 0.0f, per = 1.0f;
 
   // the 16-key halves' first cache rows (the second half may lie past the last
   // key: any row of a valid page serves), through the scalar cache
@@ -353,28 +381,33 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     }
     after_k();
 
+    float lg[8];       // far: log2 of the keys' V scales
+    bool far = false;  // (the same in every lane)
     if constexpr (FP8) {
-      // P v_scale enters the product in fp16: o in units of a power of two that
-      // bounds the scales, so that it stays at most 1
-      float vm = 0.0f;
+      float mag[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (edge) {
-          if (!inside(e)) vscale[e] = 0.0f;
-          vm = fmaxf(vm, fabsf(vscale[e]) < INFINITY ? fabsf(vscale[e]) : 0.0f);
-        } else {
-          vm = fmaxf(vm, fabsf(vscale[e]));
+        if (edge && !inside(e)) vscale[e] = 0.0f;
+        mag[e] = fabsf(vscale[e]);
+      }
+      if (bound == 0.0f) {
+        float f = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f = fmaxf(f, mag[e] < INFINITY ? mag[e] : 0.0f);
+        f = quad_max(f);
+        if (__ballot(f > 0.0f)) bound = scale_bound(f), per = 0x1p12f / bound;
+      }
+      far = edge || __ballot(scale_far(min8(mag), max8(mag), bound)) != 0;
+      if (!far) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vscale[e] *= per;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          vscale[e] = scale_units(vscale[e], per);
+          lg[e] = scale_log2_of(vscale[e]);
         }
       }
-      raise_vref(vm, vref, [&](float f) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int j = 0; j < VD; ++j) o[rt][j] *= f;
-      });
-      const float inv = 1.0f / vref;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) vscale[e] *= inv;
     }
 
     // probabilities
@@ -386,7 +419,15 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
         for (int e = 0; e < 8; ++e)
           if (!inside(e) || key_of(e) >= lim[rt]) x[rt][e] = -INFINITY;
       }
-      raise_max(max8(x[rt]) * a.scale_log2, m[rt], [&](float f) {
+      float mx;
+      if (FP8 && far) {
+        mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fmaf(x[rt][e], a.scale_log2, lg[e]));
+      } else {
+        mx = max8(x[rt]) * a.scale_log2;
+      }
+      raise_max(mx, m[rt], [&](float f) {
         l[rt] *= f;
 #pragma unroll
         for (int j = 0; j < VD; ++j) o[rt][j] *= f;
@@ -492,7 +533,9 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
   float* lo_ = lds + 4 * 64 * 2;                 // [2][VD * 4][64]
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    lml[wv * 64 + lane] = make_float2(m[rt], quad_sum(l[rt]));
+    float mw = m[rt], lw = quad_sum(l[rt]);
+    const int k = FP8 ? unit_weight(mw, lw) : 0;
+    lml[wv * 64 + lane] = make_float2(mw, lw);
     __syncthreads();
     float M = -INFINITY, L = 0.0f;
 #pragma unroll
@@ -502,10 +545,15 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
       const float2 ml = lml[w * 64 + lane];
       if (ml.x != -INFINITY) L += ml.y * __builtin_amdgcn_exp2f(ml.x - M);
     }
-    const float f =
-        (FP8 ? vref : 1.0f) * (m[rt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[rt] - M));
+    const float f = (FP8 ? 0x1p-12f * bound : 1.0f) *
+                    (mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw - M));
 #pragma unroll
-    for (int j = 0; j < VD; ++j) o[rt][j] *= f;
+    for (int j = 0; j < VD; ++j) {
+      o[rt][j] *= f;
+      if constexpr (FP8)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[rt][j][r] = __builtin_amdgcn_ldexpf(o[rt][j][r], -k);
+    }
 #pragma unroll
     for (int half = 2; half > 0; half >>= 1) {
       float* mine = lo_ + (wv % half) * (VD * 4 * 64) + lane;
@@ -629,11 +677,11 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
   constexpr int CH = D / 8;                       // 16-byte chunks of an LDS K row
   __shared__ uint4 lk[2][64][CH];
   __shared__ uint4 lv[2][D][8];                   // [column][8 chunks of 8 key slots]
-  // FP8: K scales; V scales in units of lvref, a power of two that bounds all so far
-  __shared__ float lks[2][64], lvs[2][64], lvref[2];
-  // marks by buffer: the tile (its first key) that holds a non-finite V, a bad page;
-  // whether a wave has set a group aside
-  __shared__ int lleak[2], lbad[2], lslow;
+  // FP8: K scales; V scales in units of 2^-12 lbound
+  __shared__ float lks[2][64], lvs[2][64], lbound;
+  // marks by buffer: the tile (its first key) that holds a non-finite V, a bad page, V
+  // scales far from lbound; whether a wave has set a group aside
+  __shared__ int lleak[2], lbad[2], lfar[2], lslow;
   Item itm;
   if (!item_of(a, blockIdx.x, np, itm)) return;
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -675,9 +723,7 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
 #pragma unroll
     for (int j = 0; j < VD; ++j) o[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
   }
-  // P v_scale enters the product in fp16: o in units of a power of two that bounds
-  // the scales, so that it stays small (`bound`: wave 1's, which stages them)
-  float vref = 0.0f, bound = 0x1p-100f;
+  float bound = 0.0f, per = 1.0f;  // as in attn_item (wave 1's, which stages the scales)
 
   // this thread's pieces of a tile: K piece i is 16 bytes of key kkey + i x
   // (keys per round); V unit i is columns 8 vcol.. of keys 2 vkp, 2 vkp + 1
@@ -800,11 +846,14 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
       const float v = okbits >> 31 ? sreg : 0.0f;
       const bool finite = fabsf(v) < INFINITY;
       leak |= !finite;
-      const float vm =
-          __uint_as_float(__float_as_uint(wave_max(finite ? fabsf(v) : 0.0f)) & 0x7f800000u);
-      bound = fmaxf(bound, vm + vm);
-      lvs[buf][lane] = v / bound;
-      if (lane == 0) lvref[buf] = bound;
+      if (bound == 0.0f) {
+        const float first = wave_max(finite ? fabsf(v) : 0.0f);
+        if (first > 0.0f) bound = scale_bound(first), per = 0x1p12f / bound;
+        if (lane == 0) lbound = bound;
+      }
+      if (__ballot(okbits >> 31 && scale_far(fabsf(v), fabsf(v), bound)) && lane == 0)
+        lfar[buf] = j0;
+      lvs[buf][lane] = scale_units(v, per);
     }
     if (leak) lleak[buf] = j0;
     if (badp) lbad[buf] = j0;
@@ -831,6 +880,7 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
         load_pages(j0 + 128);
       }
       const bool any_leak = lleak[buf] == j0, any_bad = lbad[buf] == j0;
+      const bool any_far = FP8 && __builtin_amdgcn_readfirstlane(lfar[buf]) == j0;
       // Where registers allow, the scores of both halves first: their products run
       // under the first half's softmax (128 columns and two row tiles: one half at a time,
       // 131 us instead of 147 for 512 rows of a kv head over 32768 keys)
@@ -885,16 +935,6 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
                 vscale[4 * u + e] = v4[e];
               }
             }
-            const float nref =
-                __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(lvref[buf])));
-            if (nref != vref) {
-              const float f = vref / nref;
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int j = 0; j < VD; ++j) o[rt][j] *= f;
-              vref = nref;
-            }
           }
           auto v_operand = [&](int j) {
             const int d = 16 * j + c;
@@ -908,14 +948,21 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
           uint4 p[RT];
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            if (edge) {
+            float mx;
+            if (edge || any_far) {
+              mx = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (key_of(e) < lo || key_of(e) >= min(hi, lim[rt]) ||
-                    (any_bad && bad_key(a, pages, key_of(e), lo, hi)))
+              for (int e = 0; e < 8; ++e) {
+                if (edge && (key_of(e) < lo || key_of(e) >= min(hi, lim[rt]) ||
+                             (any_bad && bad_key(a, pages, key_of(e), lo, hi))))
                   x[kb][rt][e] = -INFINITY;
+                mx = fmaxf(mx, fmaf(x[kb][rt][e], a.scale_log2,
+                                    FP8 ? scale_log2_of(vscale[e]) : 0.0f));
+              }
+            } else {
+              mx = max8(x[kb][rt]) * a.scale_log2;
             }
-            raise_max(max8(x[kb][rt]) * a.scale_log2, m[rt], [&](float f) {
+            raise_max(mx, m[rt], [&](float f) {
               l[rt] *= f;
 #pragma unroll
               for (int j = 0; j < VD; ++j) o[rt][j] *= f;
@@ -973,8 +1020,8 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
     }
     return aside;
   };
-  if (tid < 2) lleak[tid] = lbad[tid] = -1;
-  if (tid == 2) lslow = 0;
+  if (tid < 2) lleak[tid] = lbad[tid] = lfar[tid] = -1;
+  if (tid == 2) lslow = 0, lbound = 0.0f;
   __syncthreads();
   if (walk(std::false_type{})) lslow = 1;
   __syncthreads();
@@ -982,17 +1029,22 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     int tok, head;
-    const float lsum = quad_sum(l[rt]);
+    float lsum = quad_sum(l[rt]), mr = m[rt];
+    const int k = FP8 ? unit_weight(mr, lsum) : 0;
     if (!row_of(rt, tok, head)) continue;
     const size_t row = ((size_t)itm.part * a.n_tok + tok) * a.Hq + head;
     const bool none = lim[rt] == 0;
-    if (g == 0) a.pml[row] = make_float2(none ? -INFINITY : m[rt], none ? 0.0f : lsum);
+    if (g == 0) a.pml[row] = make_float2(none ? -INFINITY : mr, none ? 0.0f : lsum);
     float* dst = a.po + row * D + 4 * g;
-    const float f = FP8 ? vref : 1.0f;
+    const float f = FP8 ? 0x1p-12f * lbound : 1.0f;
 #pragma unroll
-    for (int j = 0; j < VD; ++j)
-      *reinterpret_cast<float4*>(dst + 16 * j) =
-          make_float4(o[rt][j][0] * f, o[rt][j][1] * f, o[rt][j][2] * f, o[rt][j][3] * f);
+    for (int j = 0; j < VD; ++j) {
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        v[r] = FP8 ? __builtin_amdgcn_ldexpf(o[rt][j][r] * f, -k) : o[rt][j][r];
+      *reinterpret_cast<float4*>(dst + 16 * j) = make_float4(v[0], v[1], v[2], v[3]);
+    }
   }
 }
 

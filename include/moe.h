@@ -418,7 +418,9 @@ size_t attn_workspace_bytes(const kv_cache* cache, int32_t n_seqs, int32_t q_len
  * A row that sees no key gives out 0 and lse -inf.  What the cache holds at keys
  * that a row does not see (NaN included) does not enter it.  A page number
  * outside the cache hides its keys and sets MOE_STATUS_BAD_PAGE.  Scores and sums
- * are fp32; probabilities are rounded to bf16 for the product with V.
+ * are fp32.  For the product with V a key's weight is rounded to bf16; in an E4M3
+ * cache the weight times the key's V scale to fp16, by 2^-11 of itself or by
+ * 2^-29 of the row's largest if that is more (V scales up to 2^80 apart).
  * n_seqs * q_len <= 262144, n_q_heads <= 1024, and n_seqs * q_len * n_q_heads
  * <= 2^24. */
 int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t n_seqs,

@@ -1,0 +1,80 @@
+"""attn_shared_prefix at values that stand out: V scales of an E4M3 cache that differ by powers
+of two.  Shapes for the blocks of 16 and 32 rows and for those over key tiles in LDS.
+Tolerances: test_gpu_attn.check, whose bound is 2^-8 of each weight, whatever the scales
+beside it."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_attn import build, call, check, positions
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [  # B, Q, Hq, Hkv, D, page, P, own
+    (3, 3, 4, 2, 64, 32, 45, [9, 40, 64]),               # blocks of 16 rows
+    (2, 4, 8, 1, 128, 64, 700, [9, 90]),
+    (20, 2, 8, 2, 128, 16, 333, list(range(2, 22))),     # shared keys: key tiles, two blocks
+    (12, 2, 8, 2, 128, 32, 140, [2 + 9 * i for i in range(12)]),   # blocks of 32 rows
+    (2, 140, 2, 1, 64, 16, 70, [140, 200]),              # both by key tiles
+    (1, 150, 2, 2, 256, 64, 130, [333]),
+]
+
+
+def make(shape, fp8, seed=0):
+    B, Q, Hq, Hkv, D, page, P, own = shape
+    rng = np.random.default_rng(seed)
+    kv, q, pre, table, n = build(rng, B, Q, Hq, Hkv, D, page, P, own, fp8)
+    return rng, kv, q, pre, table, n, positions(own, P, Q)
+
+
+def place(shape, pre, table, b, j):
+    page, P = shape[5], shape[6]
+    return int(pre[j // page] if j < P else table[b, j // page]), j % page
+
+
+def run(shape, kv, q, pos, pre, table, n):
+    Q, P, scale = shape[1], shape[6], shape[4] ** -0.5
+    o, lse = call(kv, q, pos, pre, P, table, n, scale, Q)
+    check(o, lse, q, kv, pos, pre, P, table, scale, Q, n)
+
+
+# ---- V scales
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("power", [16, 30, 100, -16, -60])
+def test_v_scale_of_a_key_some_rows_do_not_see(shape, power):
+    """The last token's key of every sequence: rows before it must not notice."""
+    rng, kv, q, pre, table, n, pos = make(shape, True)
+    print(shape, power, flush=True)
+    for b in range(shape[0]):
+        pg, s = place(shape, pre, table, b, shape[6] + shape[7][b] - 1)
+        kv.t["vs"][pg, :, s] *= 2.0 ** power
+    run(shape, kv, q, pos, pre, table, n)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("nats,power", [(64, 16), (64, 30), (14, 16), (14, 30), (300, 100), (0, 24),
+                                        (-20, -30), (-20, -14)])
+def test_v_scale_of_a_key_with_little_or_most_of_the_weight(shape, nats, power):
+    """One shared key whose score lies `nats` below (or above) the others' and whose V scale
+    is 2^power times theirs, in the first, a middle or the last key tile."""
+    print(shape, nats, power, flush=True)
+    for at in (0.0, 0.5, 1.0):
+        rng, kv, q, pre, table, n, pos = make(shape, True)
+        pg, s = place(shape, pre, table, 0, int(at * (shape[6] - 1)))
+        q[:, :, 0] = 8.0
+        if nats:
+            kv.t["k"][pg, :, s] = 0
+            kv.t["k"][pg, :, s, 0] = 0xFE if nats > 0 else 0x7E          # -+448
+            kv.t["ks"][pg, :, s] = abs(nats) / (448 * 8 * shape[4] ** -0.5)
+        kv.t["vs"][pg, :, s] *= 2.0 ** power
+        run(shape, kv, q, pos, pre, table, n)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("spread", [8, 40])
+def test_v_scales_all_different(shape, spread):
+    rng, kv, q, pre, table, n, pos = make(shape, True)
+    kv.t["vs"] *= torch.from_numpy(
+        np.exp2(rng.uniform(-spread, spread, kv.t["vs"].shape)).astype(np.float32))
+    run(shape, kv, q, pos, pre, table, n)
