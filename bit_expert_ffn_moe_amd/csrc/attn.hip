@@ -189,6 +189,13 @@ __device__ __forceinline__ void raise_max(float mx, float& m, F&& rescale) {
   }
 }
 
+// The maximum that a part's weight l goes with.  -inf says that the part holds no key (l is
+// then 0) and leaves it out; a row whose scores are all NaN has no maximum either but
+// an l of NaN, which has to reach the row's sum: beside any finite maximum it does.
+__device__ __forceinline__ float part_max(float m, float l) {
+  return m == -INFINITY && l != 0.0f ? 0.0f : m;
+}
+
 // Whether key j of the range [lo, hi) lies in a page outside the cache.
 __device__ __forceinline__ bool bad_key(const AttnArgs& a, const int32_t* pages, int j, int lo,
                                         int hi) {
@@ -535,6 +542,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
   for (int rt = 0; rt < RT; ++rt) {
     float mw = m[rt], lw = quad_sum(l[rt]);
     const int k = FP8 ? unit_weight(mw, lw) : 0;
+    mw = part_max(mw, lw);
     lml[wv * 64 + lane] = make_float2(mw, lw);
     __syncthreads();
     float M = -INFINITY, L = 0.0f;
@@ -1034,7 +1042,8 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
     if (!row_of(rt, tok, head)) continue;
     const size_t row = ((size_t)itm.part * a.n_tok + tok) * a.Hq + head;
     const bool none = lim[rt] == 0;
-    if (g == 0) a.pml[row] = make_float2(none ? -INFINITY : mr, none ? 0.0f : lsum);
+    if (g == 0)
+      a.pml[row] = make_float2(none ? -INFINITY : part_max(mr, lsum), none ? 0.0f : lsum);
     float* dst = a.po + row * D + 4 * g;
     const float f = FP8 ? 0x1p-12f * lbound : 1.0f;
 #pragma unroll

@@ -415,7 +415,8 @@ size_t attn_workspace_bytes(const kv_cache* cache, int32_t n_seqs, int32_t q_len
  *   scale: positive; o = sum_j softmax_j(scale q.k_j) v_j
  *   out [n_seqs * q_len][n_q_heads][head_dim] bf16
  *   lse [n_seqs * q_len][n_q_heads] f32 or NULL: log sum_j exp(scale q.k_j)
- * A row that sees no key gives out 0 and lse -inf.  What the cache holds at keys
+ * A row that sees no key, or none with a score above -inf, gives out 0 and lse
+ * -inf; one with a NaN score (in q, or in K at a key it sees) gives NaN.  What the cache holds at keys
  * that a row does not see (NaN included) does not enter it.  A page number
  * outside the cache hides its keys and sets MOE_STATUS_BAD_PAGE.  Scores and sums
  * are fp32.  For the product with V a key's weight is rounded to bf16; in an E4M3

@@ -1,11 +1,12 @@
 """attn_shared_prefix at values that stand out: V scales of an E4M3 cache that differ by powers
-of two.  Shapes for the blocks of 16 and 32 rows and for those over key tiles in LDS.
+of two, NaN in queries and keys.  Shapes for the blocks of 16 and 32 rows and for those over key tiles in LDS.
 Tolerances: test_gpu_attn.check, whose bound is 2^-8 of each weight, whatever the scales
 beside it."""
 import numpy as np
 import pytest
 import torch
 
+import ops_ref as ref
 from test_gpu_attn import build, call, check, positions
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +79,68 @@ def test_v_scales_all_different(shape, spread):
     kv.t["vs"] *= torch.from_numpy(
         np.exp2(rng.uniform(-spread, spread, kv.t["vs"].shape)).astype(np.float32))
     run(shape, kv, q, pos, pre, table, n)
+
+
+# ---- NaN
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan_queries_show(shape, fp8):
+    """A NaN in a query makes its own row NaN, out and lse, and no other; a padding row's
+    query may hold anything."""
+    B, Q, Hq, Hkv, D, page, P, own = shape
+    print(shape, fp8, flush=True)
+    rng, kv, q, pre, table, n, pos = make(shape, fp8)
+    pos[3] = -1
+    want = ref.attention(q.double().numpy(), kv, pos, pre, P, table, 0.125, Q, n)
+    hit = np.zeros((B * Q, Hq), bool)
+    for t, h in ((1, 0), (3, 1), (B * Q - 1, Hq - 1)):
+        q[t, h, D // 2] = float("nan")
+        hit[t, h] = t != 3
+    o, lse = call(kv, q, pos, pre, P, table, n, 0.125, Q)
+    assert np.isnan(o[hit]).all() and np.isnan(lse[hit]).all()
+    assert (o[3] == 0).all() and (lse[3] == -np.inf).all()
+    compare(o, lse, q, want, ~hit & (pos >= 0)[:, None])
+
+
+def compare(o, lse, q, want, rows):
+    """test_gpu_attn.check for some (token, head) rows, against values formed before."""
+    eo, el, mag, qk = (a[rows] for a in want)
+    d = 2 * q.shape[2] * 2.0 ** -23 * qk
+    tol = 1.05 * 2.0 ** -8 * (mag + np.abs(eo)) + (2 * d[..., None] + 2.0 ** -16) * mag
+    assert (np.abs(o[rows] - eo) <= tol).all()
+    assert (np.abs(lse[rows] - el) <= d + 2.0 ** -20 * (1 + np.abs(el))).all()
+
+
+ONLY = [  # the key spoilt is the only one of its own that the sequence's rows see, or one of many
+    (2, 1, 4, 2, 64, 16, 40, [1, 30]),
+    (1, 1, 2, 1, 128, 16, 0, [1]),
+    (40, 1, 4, 1, 128, 16, 200, [1 + i % 3 for i in range(40)]),
+    (30, 1, 4, 1, 128, 64, 0, [1 + i % 3 for i in range(30)]),
+]
+
+
+@pytest.mark.parametrize("shape", ONLY + SHAPES)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan_keys_show(shape, fp8):
+    """A NaN in K at the first own key of sequence 0: every row that sees it is NaN, out and
+    lse, the others as before; the same at a shared key."""
+    B, Q, Hq, Hkv, D, page, P, own = shape
+    print(shape, fp8, flush=True)
+    rng, kv, q, pre, table, n, pos = make(shape, fp8)
+    if Q > 1:
+        pos[1] = P // 2 if P else 0        # a row that ends before
+    want = ref.attention(q.double().numpy(), kv, pos, pre, P, table, 0.125, Q, n)
+    seq = np.arange(B * Q) // Q
+    for j, who in ((P, seq == 0), (2 * P // 3 + 1, True)):
+        if j > P or not P and who is True:
+            continue
+        pg, s = place(shape, pre, table, 0, j)
+        name = "ks" if fp8 else "k"
+        kept = kv.t[name][pg, :, s].clone()
+        kv.t[name][pg, :, s] = float("nan")
+        hit = who & (pos >= j)
+        o, lse = call(kv, q, pos, pre, P, table, n, 0.125, Q)
+        assert hit.any() and np.isnan(o[hit]).all() and np.isnan(lse[hit]).all()
+        compare(o, lse, q, want, np.repeat(~hit[:, None], Hq, 1))
+        kv.t[name][pg, :, s] = kept
