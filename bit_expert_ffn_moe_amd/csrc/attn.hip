@@ -131,7 +131,7 @@ struct Range {
 // The keys a token sees.
 __device__ __forceinline__ int row_limit(const AttnArgs& a, int t) {
   const int p = a.pos[t];
-  return p < 0 ? 0 : min(p + 1, a.max_keys);
+  return p < 0 ? 0 : min(p, a.max_keys - 1) + 1;
 }
 
 // V scales of an E4M3 cache are multiplied in units of 2^-12 `bound`, a power of two taken

@@ -1,7 +1,7 @@
 """attn_shared_prefix at values that stand out: V scales of an E4M3 cache that differ by powers
-of two, NaN in queries and keys.  Shapes for the blocks of 16 and 32 rows and for those over key tiles in LDS.
-Tolerances: test_gpu_attn.check, whose bound is 2^-8 of each weight, whatever the scales
-beside it."""
+of two, NaN in queries and keys, positions up to the largest.  Shapes for the blocks of 16 and
+32 rows and for those over key tiles in LDS.  Tolerances: test_gpu_attn.check, whose bound is
+2^-8 of each weight, whatever the scales beside it."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +10,8 @@ import ops_ref as ref
 from test_gpu_attn import build, call, check, positions
 
 pytestmark = pytest.mark.gpu
+
+import bit_expert_ffn_moe_amd as moe  # noqa: E402
 
 SHAPES = [  # B, Q, Hq, Hkv, D, page, P, own
     (3, 3, 4, 2, 64, 32, 45, [9, 40, 64]),               # blocks of 16 rows
@@ -144,3 +146,20 @@ def test_nan_keys_show(shape, fp8):
         assert hit.any() and np.isnan(o[hit]).all() and np.isnan(lse[hit]).all()
         compare(o, lse, q, want, np.repeat(~hit[:, None], Hq, 1))
         kv.t[name][pg, :, s] = kept
+
+
+# ---- positions
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_the_largest_position(shape):
+    """A position past max_keys, up to the type's last, sees the keys below max_keys."""
+    B, Q, Hq, Hkv, D, page, P, own = shape
+    rng, kv, q, pre, table, n, pos = make(shape, False)
+    b = int(np.argmax(own))                # the sequence that has all n keys
+    pos[b * Q + Q - 1] = n - 1
+    want = call(kv, q, pos, pre, P, table, n, 0.1, Q)
+    check(*want, q, kv, pos, pre, P, table, 0.1, Q, n)
+    for p in (n, 2 ** 31 - 1):
+        pos[b * Q + Q - 1] = p
+        got = call(kv, q, pos, pre, P, table, n, 0.1, Q, expect_status=moe.MOE_STATUS_BAD_PAGE)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]), p
