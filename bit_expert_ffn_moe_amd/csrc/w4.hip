@@ -414,6 +414,25 @@ __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4
 #pragma unroll
           for (int i = 0; i < S; ++i) gs[i] = ue8m0_operand(cur.sc[i]);
         }
+        // FP4: 6 x 2^126 and more is past bf16.  A row with such a scale is converted at a
+        // quarter and its sums, of this lane's row alone, are multiplied by 4 again.
+        bool large = false;
+        float back = 1.0f;
+        if constexpr (!INT4) {
+          float top = gs[0];
+#pragma unroll
+          for (int i = 1; i < S; ++i) top = fmaxf(top, gs[i]);
+          large = __ballot(top >= 0x1p126f) != 0;
+          if (large) {
+            top = fmaxf(top, xchg16(top));  // over the row's lane groups
+            top = fmaxf(top, xchg32(top));
+            if (top >= 0x1p126f) {
+              back = 4.0f;
+#pragma unroll
+              for (int i = 0; i < S; ++i) gs[i] *= 0.25f;
+            }
+          }
+        }
         v4f_t acc[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) acc[t] = v4f_t{0.f, 0.f, 0.f, 0.f};
@@ -472,6 +491,10 @@ __global__ __launch_bounds__(64 * kW4Waves, kW4Waves / 4) void w4_mfma_kernel(W4
           }
         }
         if (MORE || it + DEPTH < n_it) load_tile(it + DEPTH, cur);
+        if (large) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t) acc[t] *= back;
+        }
         if (pending >= 0) join(pending, rv);
 #pragma unroll
         for (int t = 0; t < TT; ++t)
