@@ -44,6 +44,12 @@ __device__ __forceinline__ void unpack8(const uint4 r, float (&v)[8]) {
   }
 }
 
+// 0x7f, E4M3's NaN, in the byte of each of four values that is NaN.
+__device__ __forceinline__ uint32_t nan_bytes(const float* v) {
+  return (v[0] != v[0] ? 0x7fu : 0u) | (v[1] != v[1] ? 0x7f00u : 0u) |
+         (v[2] != v[2] ? 0x7f0000u : 0u) | (v[3] != v[3] ? 0x7f000000u : 0u);
+}
+
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
                     f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
@@ -137,6 +143,10 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
         q.x = e4m3_pack4(v[0] / sc, v[1] / sc, v[2] / sc, v[3] / sc);
         q.y = e4m3_pack4(v[4] / sc, v[5] / sc, v[6] / sc, v[7] / sc);
       }
+      // a NaN keeps its place (the maximum and the conversion's clamp pass over it)
+      const uint2 nan = make_uint2(nan_bytes(v), nan_bytes(v + 4));
+      if (__ballot((nan.x | nan.y) != 0))
+        q = make_uint2((q.x & ~(nan.x << 1)) | nan.x, (q.y & ~(nan.y << 1)) | nan.y);
       *reinterpret_cast<uint2*>(dst + row * D + 8 * c) = q;
       if (c == 0) (is_v ? a.vs : a.ks)[row] = sc;
     }

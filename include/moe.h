@@ -374,7 +374,9 @@ enum { MOE_ROPE_HALF = 1, MOE_ROPE_PAIRS = 2 };
  * the first rope_dim elements of a head becomes (a c - b s, b c + a s) in fp32,
  * each operation rounded, with c = rope[pos][i], s = rope[pos][rope_dim/2 + i];
  * the other elements and v are taken as they are.  Cache rows are bf16 (nearest
- * even), or E4M3 by the rule of act_quant_fp8 over the whole head row.
+ * even), or E4M3 by the rule of act_quant_fp8 over the whole head row, where a NaN
+ * becomes E4M3's NaN and leaves the row's other values as they are; an infinity
+ * leaves the row no finite value (scale inf).
  *   q [T][n_q_heads][head_dim] bf16, token rows q_stride apart; n_q_heads = 0
  *     (q, q_out NULL): keys and values only
  *   k, v [T][n_kv_heads][head_dim] bf16, token rows k_stride, v_stride apart
