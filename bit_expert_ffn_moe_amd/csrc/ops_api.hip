@@ -87,8 +87,10 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   if (n_seqs < 0 || q_len < 1 || n_q_heads < 1 || n_q_heads % c->n_kv_heads) return MOE_EINVAL;
   if (prefix_len < 0 || max_keys < 1 || prefix_len > max_keys) return MOE_EINVAL;
   if (n_q_heads > 1024 || (int64_t)n_seqs * q_len > kMaxT ||
-      (int64_t)n_seqs * q_len * n_q_heads > (1 << 24) || max_keys > (1 << 28))
+      (int64_t)n_seqs * q_len * n_q_heads >= (1 << 24) || max_keys > (1 << 28))
     return MOE_ENOTSUP;
+  // (a launch has at most a block of 256 threads per row, or about `want` below: with 2^24
+  // rows that would be more threads than a grid holds)
   memset(a, 0, sizeof *a);
   a->B = n_seqs, a->Q = q_len, a->n_tok = n_seqs * q_len;
   a->Hq = n_q_heads, a->Hkv = c->n_kv_heads, a->G = n_q_heads / c->n_kv_heads, a->D = c->head_dim;
@@ -109,9 +111,6 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   split_keys(max_keys > prefix_len ? max_keys - (prefix_len & ~31) : 0, a->own_kind,
              a->B * a->Hkv * a->own_blocks, want - taken < want_p ? want_p : want - taken,
              &a->own_chunk, &a->n_own_parts);
-  const int64_t items = (int64_t)a->n_prefix_parts * a->Hkv * a->prefix_blocks +
-                        (int64_t)a->n_own_parts * a->B * a->Hkv * a->own_blocks;
-  if (items > 0x7fffffff) return MOE_ENOTSUP;
   return MOE_OK;
 }
 

@@ -418,14 +418,15 @@ size_t attn_workspace_bytes(const kv_cache* cache, int32_t n_seqs, int32_t q_len
  *   out [n_seqs * q_len][n_q_heads][head_dim] bf16
  *   lse [n_seqs * q_len][n_q_heads] f32 or NULL: log sum_j exp(scale q.k_j)
  * A row that sees no key, or none with a score above -inf, gives out 0 and lse
- * -inf; one with a NaN score (in q, or in K at a key it sees) gives NaN.  What the cache holds at keys
- * that a row does not see (NaN included) does not enter it.  A page number
- * outside the cache hides its keys and sets MOE_STATUS_BAD_PAGE.  Scores and sums
- * are fp32.  For the product with V a key's weight is rounded to bf16; in an E4M3
- * cache the weight times the key's V scale to fp16, by 2^-11 of itself or by
- * 2^-29 of the row's largest if that is more (V scales up to 2^80 apart).
- * n_seqs * q_len <= 262144, n_q_heads <= 1024, and n_seqs * q_len * n_q_heads
- * <= 2^24. */
+ * -inf; one with a NaN score (in q, or in K at a key it sees) gives NaN.  What the
+ * cache holds at keys that a row does not see (NaN included) does not enter it.  A
+ * page number outside the cache hides its keys and sets MOE_STATUS_BAD_PAGE.
+ * Scores and sums are fp32.  For the product with V a key's weight is rounded to
+ * bf16; in an E4M3 cache the weight times the key's V scale to fp16, by 2^-11 of
+ * itself or by 2^-29 of the row's largest if that is more (V scales up to 2^80
+ * apart).
+ * n_seqs * q_len <= 262144, n_q_heads <= 1024, n_seqs * q_len * n_q_heads < 2^24
+ * and max_keys <= 2^28. */
 int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t n_seqs,
                        int32_t q_len, int32_t n_q_heads, const int32_t* pos,
                        const int32_t* prefix_pages, int32_t prefix_len, const int32_t* page_table,
