@@ -163,3 +163,23 @@ def test_the_largest_position(shape):
         pos[b * Q + Q - 1] = p
         got = call(kv, q, pos, pre, P, table, n, 0.1, Q, expect_status=moe.MOE_STATUS_BAD_PAGE)
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]), p
+
+
+# ---- V scales of 0
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_v_scales_of_zero(shape):
+    """Rows of zeros in V, as appended: a key of most of the weight, every shared key, all."""
+    print(shape, flush=True)
+    for nats in (20, 40, 60):
+        rng, kv, q, pre, table, n, pos = make(shape, True)
+        q[:, :, 0] = 8.0
+        pg, s = place(shape, pre, table, 0, shape[6] // 2)
+        kv.t["k"][pg, :, s] = 0
+        kv.t["k"][pg, :, s, 0] = 0x7E
+        kv.t["ks"][pg, :, s] = nats / (448 * 8 * shape[4] ** -0.5)
+        kv.t["v"][pg, :, s], kv.t["vs"][pg, :, s] = 0, 0.0
+        run(shape, kv, q, pos, pre, table, n)
+    for pages in (torch.from_numpy(np.asarray(pre)), slice(None)):
+        kv.t["v"][pages], kv.t["vs"][pages] = 0, 0.0
+        run(shape, kv, q, pos, pre, table, n)
