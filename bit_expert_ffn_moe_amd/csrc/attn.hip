@@ -28,10 +28,10 @@
 // row does not see or gives no weight, takes nothing from the weights beside it.
 //
 // Measured at 128 columns, bf16, 32 sequences of 8 kv heads and 4 query heads each:
-// 8192 shared keys and up to 2048 of their own, 161 MB, in 44 us with the join (3.7
-// TB/s: the shared keys are read by four blocks of rows, from L2 but for the
+// 8192 shared keys and up to 2048 of their own, 161 MB, in 47 us and 5 for the join (3.1
+// TB/s in all: the shared keys are read by four blocks of rows, from L2 but for the
 // first).  16 sequences of 4 tokens, 8 kv heads of 8 query heads each, 32768 shared
-// E4M3 keys and up to 1024 of their own, 70 GFLOP: 136 us.
+// E4M3 keys and up to 1024 of their own, 70 GFLOP: 133 us.
 #include <type_traits>
 
 #include "common.h"
@@ -673,8 +673,8 @@ __global__ __launch_bounds__(256, D < 256 && RTP == 1 ? 3 : 2) void attn_part_ke
 //
 // Bound by the vector unit (a score costs an exponential and six more operations, with
 // an FP8 cache's two scales) and the matrix cores in turn: 512 rows of 8 kv heads
-// over 32768 keys, 69 GFLOP, 114 us bf16 with the join, 120 us FP8 without it, the
-// matrix cores busy for 26% of that.  (Forming the scores of the next 32 keys
+// over 32768 keys, 69 GFLOP, 114 us bf16 with the join, 113 us FP8 without it, the
+// matrix cores busy for 27% of that.  (Forming the scores of the next 32 keys
 // under the exponentials of these takes the registers that hide LDS and loads: 170
 // us bf16.)
 template <int D, bool FP8, int RT>

@@ -14,8 +14,8 @@
 // joins them itself: bound by HBM and, closely, by the vector unit (an
 // exponential and ten more operations an element).
 // Measured: one row of 131072 fp32 with its 20 best 12.8 us, 32 rows of bf16 with 5
-// 14.8 us (two launches and their latencies); 4096 rows of 50021 bf16, 410 MB, 86 us
-// (4.8 TB/s).
+// 14.8 us (two launches and their latencies); 4096 rows of 50021 bf16, 410 MB, 82 to 86
+// us (4.8 to 5.0 TB/s).
 //
 // A candidate is one 64-bit key: the logit's order in the high word (a
 // monotone map of fp32 to unsigned, NaN 1 and below every number, 0 for places

@@ -339,7 +339,8 @@ typedef struct w4_weights {
 
 /* y[t][n] = sum_k x[t][k] w[n][k]: the projections around the expert layer for
  * a few tokens (any T is valid; tuned up to 64).  Codes and activations
- * enter the products unrounded, sums are fp32, y is rounded once.
+ * enter the products unrounded, sums are fp32, y is rounded once.  (INT4 sums
+ * code x and x apart, so an infinite activation gives NaN in its token.)
  *   x [T][n_in] bf16, rows x_stride apart (a multiple of 8, >= n_in)
  *   y [T][n_out] bf16 or f32 (y_dtype), rows y_stride >= n_out apart
  * n_out and n_in up to 2^20 (MOE_ENOTSUP beyond). */
