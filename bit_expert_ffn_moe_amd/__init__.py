@@ -22,7 +22,7 @@ MOE_OK, MOE_EINVAL, MOE_ENOTSUP, MOE_EALIGN, MOE_EWORKSPACE, MOE_ELAUNCH = 0, -1
 MOE_W_FP4_E2M1_UE8M0_K32, MOE_W_FP8_E4M3_F32_B128, MOE_W_INT4_BF16_GROUP = 1, 2, 3
 MOE_DT_BF16, MOE_DT_F32, MOE_DT_FP8_E4M3 = 1, 2, 3
 MOE_STATUS_BAD_EXPERT_ID, MOE_STATUS_SYNC_TIMEOUT = 1, 2
-MOE_STATUS_BAD_PAGE, MOE_STATUS_BAD_TOKEN = 4, 8
+MOE_STATUS_BAD_PAGE, MOE_STATUS_BAD_TOKEN, MOE_STATUS_BAD_INDEX = 4, 8, 16
 ROPE_HALF = MOE_ROPE_HALF = 1
 ROPE_PAIRS = MOE_ROPE_PAIRS = 2
 MOE_KERNEL_GEMV_GATE_UP, MOE_KERNEL_GEMM_GATE_UP, MOE_KERNEL_GEMV_DOWN, MOE_KERNEL_GEMM_DOWN = 1, 2, 3, 4
@@ -79,11 +79,31 @@ class kv_cache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p)]
 
 
+class lora_weights(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
+                ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32), ("a", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("rank", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class logits_rules(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64),
+                ("max_history", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("seq_of", ctypes.c_void_p), ("n_tokens", ctypes.c_void_p),
+                ("n_prompt", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+                ("mask_of", ctypes.c_void_p), ("n_masks", ctypes.c_int32),
+                ("n_bias", ctypes.c_int32)]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _W = ctypes.POINTER(moe_weights)
 _C = ctypes.POINTER(moe_expert_cache)
 _L = ctypes.POINTER(w4_weights)
 _KV = ctypes.POINTER(kv_cache)
+_LA = ctypes.POINTER(lora_weights)
+_LR = ctypes.POINTER(logits_rules)
 _sigs = {
     "moe_workspace_bytes": ([_W, _i32, _i32], _sz),
     "moe_workspace_init": ([_vp, _sz, _vp], ctypes.c_int),
@@ -112,6 +132,12 @@ _sigs = {
     "token_logprobs_workspace_bytes": ([_i32, _i32, _i32], _sz),
     "token_logprobs": ([_vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                         _vp], ctypes.c_int),
+    "lora_workspace_bytes": ([_LA, _i32], _sz),
+    "lora_linear": ([_LA, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _sz, _vp],
+                    ctypes.c_int),
+    "add_rmsnorm": ([_vp, _i64, _vp, _i32, _i64, _i32, _i32, _vp, ctypes.c_float, _vp, _vp, _vp,
+                     _vp, _vp], ctypes.c_int),
+    "logits_adjust": ([_LR, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _i64, _vp, _vp], ctypes.c_int),
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "moe_device_status": ([_vp, _vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int],
                           ctypes.c_int),
@@ -284,6 +310,32 @@ def w4_linear(w, x, x_stride, T, y, y_stride, y_dtype, stream=None) -> int:
                                  _stream(stream)), "w4_linear")
 
 
+def make_lora(n_adapters, max_rank, n_in, n_out, a, b, rank=None, scale=None):
+    """Build the C descriptor of a linear's stacked low-rank adapters from device
+    buffers (ints or tensors).  The returned object keeps references to tensors."""
+    w = lora_weights(n_adapters, max_rank, n_in, n_out, _ptr(a), _ptr(b), _ptr(rank), _ptr(scale))
+    w._keep = (a, b, rank, scale)
+    return w
+
+
+def lora_workspace_bytes(w, T) -> int:
+    return _lib.lora_workspace_bytes(ctypes.byref(w), T)
+
+
+def lora_linear(w, x, x_stride, T, adapter_of, base, base_stride, y, y_stride, y_dtype, status, ws,
+                ws_bytes, stream=None) -> int:
+    return _check(_lib.lora_linear(
+        ctypes.byref(w), _ptr(x), x_stride, T, _ptr(adapter_of), _ptr(base), base_stride, _ptr(y),
+        y_stride, y_dtype, _ptr(status), _ptr(ws), ws_bytes, _stream(stream)), "lora_linear")
+
+
+def add_rmsnorm(x, x_stride, residual, res_dtype, res_stride, T, H, weight, eps, res_out, y, q,
+                scales, stream=None) -> int:
+    return _check(_lib.add_rmsnorm(
+        _ptr(x), x_stride, _ptr(residual), res_dtype, res_stride, T, H, _ptr(weight), eps,
+        _ptr(res_out), _ptr(y), _ptr(q), _ptr(scales), _stream(stream)), "add_rmsnorm")
+
+
 def make_kv_cache(dtype, n_pages, page_size, n_kv_heads, head_dim, k, v, k_scale=None,
                   v_scale=None):
     """Build the C descriptor of a paged key/value cache from device buffers
@@ -315,6 +367,28 @@ def attn_shared_prefix(cache, q, q_stride, n_seqs, q_len, n_q_heads, pos, prefix
         ctypes.byref(cache), _ptr(q), q_stride, n_seqs, q_len, n_q_heads, _ptr(pos),
         _ptr(prefix_pages), prefix_len, _ptr(page_table), table_cols, max_keys, scale, _ptr(out),
         _ptr(lse), _ptr(status), _ptr(ws), ws_bytes, _stream(stream)), "attn_shared_prefix")
+
+
+def make_logits_rules(history=None, history_stride=0, max_history=0, n_seqs=0, seq_of=None,
+                      n_tokens=None, n_prompt=None, repetition=None, presence=None,
+                      frequency=None, bias_ids=None, bias=None, n_bias=0, mask=None, mask_stride=0,
+                      n_masks=0, mask_of=None):
+    """Build the C descriptor of rules on logits from device buffers (ints or
+    tensors).  The returned object keeps references to tensors."""
+    r = logits_rules(_ptr(history), history_stride, max_history, n_seqs, _ptr(seq_of),
+                     _ptr(n_tokens), _ptr(n_prompt), _ptr(repetition), _ptr(presence),
+                     _ptr(frequency), _ptr(bias_ids), _ptr(bias), _ptr(mask), mask_stride,
+                     _ptr(mask_of), n_masks, n_bias)
+    r._keep = (history, seq_of, n_tokens, n_prompt, repetition, presence, frequency, bias_ids, bias,
+               mask, mask_of)
+    return r
+
+
+def logits_adjust(rules, z, z_dtype, z_stride, T, V, out, out_dtype, out_stride, status,
+                  stream=None) -> int:
+    return _check(_lib.logits_adjust(
+        ctypes.byref(rules), _ptr(z), z_dtype, z_stride, T, V, _ptr(out), out_dtype, out_stride,
+        _ptr(status), _stream(stream)), "logits_adjust")
 
 
 def token_logprobs_workspace_bytes(T, V, n_top) -> int:

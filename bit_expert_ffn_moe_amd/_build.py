@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 SO = os.path.join(PKG, "libbefmoe.so")
 SOURCES = ["moe_api.hip", "actq.hip", "route.hip", "permute.hip", "gemv.hip", "gemm.hip",
            "combine.hip", "decode.hip", "ops_api.hip", "w4.hip", "kv.hip", "attn.hip",
-           "logprobs.hip"]
+           "logprobs.hip", "norm.hip", "logits.hip",
+           "lora.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -166,6 +166,61 @@ struct W4Args {
 };
 hipError_t launch_w4(const W4Args& a, hipStream_t st);
 
+// Low-rank adapters beside a linear (lora.hip).
+struct LoraArgs {
+  const uint16_t *a, *b;   // [n][R][K], [n][N][R]
+  const int32_t* rank;     // or null (R)
+  const float* scale;      // or null (1)
+  const uint16_t* x;
+  const int32_t* of;
+  const void* base;        // or null
+  void* y;
+  float* h;                // [parts][T][R] partial sums of a x
+  uint32_t* status;
+  int64_t x_stride, base_stride, y_stride;
+  int T, K, N, R, n, parts, steps;  // steps: of 32 columns a wave takes at a time (1, 2, 4, 8)
+  int part_cols;           // columns of x in a part
+  bool y_bf16, in_place;
+};
+hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
+
+// Residual's addition and root-mean-square norm (norm.hip).
+struct NormArgs {
+  const uint16_t* x;
+  const void* res;         // null: none
+  void* res_out;
+  const uint16_t* w;       // null: 1
+  uint16_t* y;
+  uint8_t* q;
+  float* qs;
+  int64_t x_stride, res_stride;
+  float eps;
+  int T, H;
+  bool res_f32;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t st);
+
+// Rules on logits (logits.hip).
+struct LogitsArgs {
+  const void* z;
+  void* out;
+  int64_t z_stride, out_stride;
+  int T, V;
+  const int32_t *history, *seq_of, *n_tokens, *n_prompt;
+  int64_t history_stride;
+  int max_history, n_seqs;
+  const float *repetition, *presence, *frequency;
+  const int32_t* bias_ids;
+  const float* bias;
+  int n_bias, n_masks;
+  const uint32_t* mask;
+  int64_t mask_stride;
+  const int32_t* mask_of;
+  uint32_t* status;
+  bool z_bf16, out_bf16, in_place;
+};
+hipError_t launch_logits(const LogitsArgs& a, hipStream_t st);
+
 // Paged cache append with rotation (kv.hip).
 struct KvAppendArgs {
   void *kc, *vc;

@@ -156,6 +156,31 @@ int check_logprobs(int T, int V, int n_top) {
   return MOE_OK;
 }
 
+int check_lora(const lora_weights* w) {
+  if (!w || !w->a || !w->b || w->n_adapters < 1 || w->max_rank < 8 || w->max_rank % 8 ||
+      w->n_in < 8 || w->n_in % 8 || w->n_out < 1)
+    return MOE_EINVAL;
+  if (w->n_adapters > 65536 || w->max_rank > 128 || w->n_in > (1 << 20) || w->n_out > (1 << 20))
+    return MOE_ENOTSUP;
+  if (!aligned(w->a, 16) || !aligned(w->b, 16) || !aligned(w->rank, 4) || !aligned(w->scale, 4))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+// How the columns of x are dealt out: a block of 8 waves takes 256 `steps` of them at a
+// time.  Few tokens: small pieces over many blocks; many: long ones, whose partial sums
+// are fewer.
+void lora_split(int T, int K, int n_adapters, int* steps, int* part_cols, int* parts) {
+  const int tiles = ceil_div(T, 16);
+  int slots = T < 16 ? T : 16;
+  if (slots > n_adapters) slots = n_adapters;
+  int s = 8;
+  while (s > 1 && (int64_t)tiles * slots * ceil_div(K, 256 * s) < 256) s >>= 1;
+  const int pieces = ceil_div(K, 256 * s);
+  const int each = ceil_div(pieces, 16);
+  *steps = s, *part_cols = each * 256 * s, *parts = ceil_div(pieces, each);
+}
+
 }  // namespace
 
 extern "C" {
@@ -189,6 +214,115 @@ int w4_linear(const w4_weights* w, const uint16_t* x, int64_t x_stride, int32_t 
   return launch_status(launch_w4(a, (hipStream_t)stream));
 }
 
+size_t lora_workspace_bytes(const lora_weights* w, int32_t T) {
+  if (check_lora(w) || T < 1 || T > kMaxT) return 0;
+  int steps, cols, parts;
+  lora_split(T, w->n_in, w->n_adapters, &steps, &cols, &parts);
+  return up256((size_t)parts * T * w->max_rank * 4);
+}
+
+int lora_linear(const lora_weights* w, const uint16_t* x, int64_t x_stride, int32_t T,
+                const int32_t* adapter_of, const void* base, int64_t base_stride, void* y,
+                int64_t y_stride, int32_t y_dtype, uint32_t* status, void* ws, size_t ws_bytes,
+                void* stream) {
+  int rc = check_lora(w);
+  if (rc) return rc;
+  if (!x || !adapter_of || !y || T < 0) return MOE_EINVAL;
+  if (y_dtype != MOE_DT_BF16 && y_dtype != MOE_DT_F32) return MOE_EINVAL;
+  if (check_rows(x_stride, w->n_in) || y_stride < w->n_out || y_stride > ((int64_t)1 << 40))
+    return MOE_EINVAL;
+  if (base && (base_stride < w->n_out || base_stride > ((int64_t)1 << 40))) return MOE_EINVAL;
+  if (base == y && base_stride != y_stride) return MOE_EINVAL;
+  if (T > kMaxT) return MOE_ENOTSUP;
+  if (!aligned(x, 16) || !aligned(base, 16) || !aligned(y, 16) || !aligned(adapter_of, 4) ||
+      !aligned(status, 4))
+    return MOE_EALIGN;
+  if (T == 0) return MOE_OK;
+  if (!ws) return MOE_EINVAL;
+  if (!aligned(ws, 256)) return MOE_EALIGN;
+  if (ws_bytes < lora_workspace_bytes(w, T)) return MOE_EWORKSPACE;
+  rc = check_device();
+  if (rc) return rc;
+  LoraArgs a;
+  memset(&a, 0, sizeof a);
+  a.a = (const uint16_t*)w->a, a.b = (const uint16_t*)w->b, a.rank = w->rank, a.scale = w->scale;
+  a.x = x, a.of = adapter_of, a.base = base, a.y = y, a.h = (float*)ws, a.status = status;
+  a.x_stride = x_stride, a.base_stride = base_stride, a.y_stride = y_stride;
+  a.T = T, a.K = w->n_in, a.N = w->n_out, a.R = w->max_rank, a.n = w->n_adapters;
+  a.y_bf16 = y_dtype == MOE_DT_BF16, a.in_place = base == y;
+  lora_split(T, a.K, a.n, &a.steps, &a.part_cols, &a.parts);
+  return launch_status(launch_lora(a, (hipStream_t)stream));
+}
+
+int add_rmsnorm(const uint16_t* x, int64_t x_stride, const void* residual, int32_t res_dtype,
+                int64_t res_stride, int32_t T, int32_t H, const uint16_t* weight, float eps,
+                void* res_out, uint16_t* y, uint8_t* q, float* scales, void* stream) {
+  if (!x || (!y && !q) || (q != nullptr) != (scales != nullptr)) return MOE_EINVAL;
+  if (residual ? res_dtype != MOE_DT_BF16 && res_dtype != MOE_DT_F32 : res_out != nullptr)
+    return MOE_EINVAL;
+  if (T < 0 || H < 8 || H % 8 || (q && H % 128)) return MOE_EINVAL;
+  if (check_rows(x_stride, H) || (residual && check_rows(res_stride, H))) return MOE_EINVAL;
+  if (!(eps >= 0x1p-100f) || !isfinite(eps)) return MOE_EINVAL;
+  if (T > kMaxT || H > 16384) return MOE_ENOTSUP;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(res_out, 16) ||
+      !aligned(y, 16) || !aligned(q, 16) || !aligned(scales, 16))
+    return MOE_EALIGN;
+  if (T == 0) return MOE_OK;
+  int rc = check_device();
+  if (rc) return rc;
+  NormArgs a;
+  memset(&a, 0, sizeof a);
+  a.x = x, a.res = residual, a.res_out = res_out, a.w = weight, a.y = y, a.q = q, a.qs = scales;
+  a.x_stride = x_stride, a.res_stride = res_stride, a.eps = eps, a.T = T, a.H = H;
+  a.res_f32 = residual && res_dtype == MOE_DT_F32;
+  return launch_status(launch_norm(a, (hipStream_t)stream));
+}
+
+int logits_adjust(const logits_rules* r, const void* z, int32_t z_dtype, int64_t z_stride,
+                  int32_t T, int32_t V, void* out, int32_t out_dtype, int64_t out_stride,
+                  uint32_t* status, void* stream) {
+  if (!r || !z || !out) return MOE_EINVAL;
+  if (z_dtype != MOE_DT_BF16 && z_dtype != MOE_DT_F32) return MOE_EINVAL;
+  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32) return MOE_EINVAL;
+  if (T < 0 || V < 1 || z_stride < V || z_stride > ((int64_t)1 << 40) || out_stride < V ||
+      out_stride > ((int64_t)1 << 40))
+    return MOE_EINVAL;
+  if (z == out && (z_dtype != out_dtype || z_stride != out_stride)) return MOE_EINVAL;
+  if (r->history ? !r->n_tokens || r->n_seqs < 1 || r->max_history < 1 ||
+                       r->history_stride < r->max_history ||
+                       r->history_stride > ((int64_t)1 << 40)
+                 : r->repetition || r->presence || r->frequency)
+    return MOE_EINVAL;
+  if (r->n_bias < 0 || (r->n_bias > 0) != (r->bias_ids != nullptr) ||
+      (r->n_bias > 0) != (r->bias != nullptr))
+    return MOE_EINVAL;
+  if (r->mask && (r->n_masks < 1 || r->mask_stride < ((int64_t)V + 31) / 32 ||
+                  r->mask_stride > ((int64_t)1 << 40)))
+    return MOE_EINVAL;
+  if (T > kMaxT || V > (1 << 24) || (r->history && r->max_history >= (1 << 20)) || r->n_bias > 2047)
+    return MOE_ENOTSUP;
+  if (!aligned(z, z_dtype == MOE_DT_BF16 ? 2 : 4) || !aligned(out, out_dtype == MOE_DT_BF16 ? 2 : 4) ||
+      !aligned(r->history, 4) || !aligned(r->seq_of, 4) || !aligned(r->n_tokens, 4) ||
+      !aligned(r->n_prompt, 4) || !aligned(r->repetition, 4) || !aligned(r->presence, 4) ||
+      !aligned(r->frequency, 4) || !aligned(r->bias_ids, 4) || !aligned(r->bias, 4) ||
+      !aligned(r->mask, 4) || !aligned(r->mask_of, 4) || !aligned(status, 4))
+    return MOE_EALIGN;
+  if (T == 0) return MOE_OK;
+  int rc = check_device();
+  if (rc) return rc;
+  LogitsArgs a;
+  memset(&a, 0, sizeof a);
+  a.z = z, a.out = out, a.z_stride = z_stride, a.out_stride = out_stride, a.T = T, a.V = V;
+  a.history = r->history, a.seq_of = r->seq_of, a.n_tokens = r->n_tokens, a.n_prompt = r->n_prompt;
+  a.history_stride = r->history_stride, a.max_history = r->max_history, a.n_seqs = r->n_seqs;
+  a.repetition = r->repetition, a.presence = r->presence, a.frequency = r->frequency;
+  a.bias_ids = r->bias_ids, a.bias = r->bias, a.n_bias = r->n_bias;
+  a.mask = r->mask, a.mask_stride = r->mask_stride, a.mask_of = r->mask_of, a.n_masks = r->n_masks;
+  a.status = status, a.in_place = z == out;
+  a.z_bf16 = z_dtype == MOE_DT_BF16, a.out_bf16 = out_dtype == MOE_DT_BF16;
+  return launch_status(launch_logits(a, (hipStream_t)stream));
+}
+
 int kv_append_rope(const kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,
                    const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
                    int32_t T, const float* rope, int32_t rope_rows, int32_t rope_dim,
@@ -220,7 +354,7 @@ int kv_append_rope(const kv_cache* cache, const uint16_t* q, int64_t q_stride, i
   if (rc) return rc;
   KvAppendArgs a;
   memset(&a, 0, sizeof a);
-  a.kc = cache->k, a.vc = cache->v, a.ks = cache->k_scale, a.vs = cache->v_scale;
+  a.kc = cache->k, a.vc = cache->v, a.ks = (float*)cache->k_scale, a.vs = (float*)cache->v_scale;
   a.q = q, a.k = k, a.v = v, a.q_out = q_out;
   a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
   a.rope = rope, a.seq_of = seq_of, a.pos = pos, a.table = page_table, a.status = status;
@@ -262,7 +396,7 @@ int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_strid
   if (ws_bytes < attn_bytes(a)) return MOE_EWORKSPACE;
   rc = check_device();
   if (rc) return rc;
-  a.k = cache->k, a.v = cache->v, a.ks = cache->k_scale, a.vs = cache->v_scale;
+  a.k = cache->k, a.v = cache->v, a.ks = (float*)cache->k_scale, a.vs = (float*)cache->v_scale;
   a.q = q, a.q_stride = q_stride, a.pos = pos, a.prefix_pages = prefix_pages;
   a.table = page_table, a.table_cols = table_cols;
   a.out = out, a.lse = lse, a.status = status;

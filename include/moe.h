@@ -1,7 +1,9 @@
 /*
  * moe.h -- C ABI of the MI355X (gfx950) routed-expert MoE FFN library, and
- * of the operators that surround the layer in a decode step (4-bit linears,
- * a paged key/value cache, attention over it, token log probabilities).
+ * of the operators that surround the layer in a decode step (4-bit linears
+ * with low-rank adapters beside them, norms with the residual's addition, a
+ * paged key/value cache, attention over it, rules on logits, token log
+ * probabilities).
  *
  * The layer: 256 routed experts, top-6 per token, plus one always-on shared
  * expert (tcti.cn post on DeepSeek-V4-Flash on 4x RTX 2080 Ti, section
@@ -84,7 +86,7 @@ enum { MOE_STATUS_BAD_EXPERT_ID = 1u, MOE_STATUS_SYNC_TIMEOUT = 2u };
 
 /* Bits that the decode-step operators OR into the caller's `status` word (a
  * device uint32_t, 4-byte aligned, cleared by the caller; NULL: not reported). */
-enum { MOE_STATUS_BAD_PAGE = 4u, MOE_STATUS_BAD_TOKEN = 8u };
+enum { MOE_STATUS_BAD_PAGE = 4u, MOE_STATUS_BAD_TOKEN = 8u, MOE_STATUS_BAD_INDEX = 16u };
 
 /* Stacked expert weights, expert-major; slot E (the last) is the shared
  * expert, which must have the same intermediate size as the routed ones.
@@ -347,6 +349,66 @@ typedef struct w4_weights {
 int w4_linear(const w4_weights* w, const uint16_t* x, int64_t x_stride, int32_t T, void* y,
               int64_t y_stride, int32_t y_dtype, void* stream);
 
+/* Low-rank adapters of one linear, n_adapters of them stacked:
+ *   a [n_adapters][max_rank][n_in] bf16, b [n_adapters][n_out][max_rank] bf16
+ *   rank [n_adapters] int32 (device), 0 to max_rank, or NULL (all max_rank): what a
+ *     and b hold past an adapter's rank is not used
+ *   scale [n_adapters] f32 (device) or NULL (1)
+ * max_rank and n_in are multiples of 8, max_rank up to 128, n_in and n_out up to
+ * 2^20, n_adapters up to 65536 (MOE_ENOTSUP beyond).  The descriptor is host memory,
+ * read during the call only. */
+typedef struct lora_weights {
+  int32_t n_adapters;
+  int32_t max_rank;
+  int32_t n_in;
+  int32_t n_out;
+  const void* a;
+  const void* b;
+  const int32_t* rank;
+  const float* scale;
+} lora_weights;
+
+/* Workspace bytes of lora_linear for T tokens (0 on invalid arguments). */
+size_t lora_workspace_bytes(const lora_weights* w, int32_t T);
+
+/* y[t] = base[t] + scale_i b_i (a_i x[t]) with i = adapter_of[t]: the adapters of many
+ * requests beside a projection that they share (base: what w4_linear or another
+ * product left).  a_i x is kept in fp32, both products accumulate in fp32, y is
+ * rounded once.  (a_i x meets b_i in three bf16 parts that add up to it, so an
+ * infinite element of b gives NaN.)
+ *   x [T][n_in] bf16, rows x_stride apart (a multiple of 8, >= n_in)
+ *   adapter_of [T] int32; negative: none (y = base).  An index >= n_adapters is none
+ *     too and sets MOE_STATUS_BAD_INDEX.  Tokens of one adapter need not be
+ *     neighbours; runs of 16 or more of them read its weights less often.
+ *   base [T][n_out], rows base_stride apart, of y's type; NULL: zeros.  base may be y,
+ *     with y's stride; otherwise they must not overlap
+ *   y [T][n_out] bf16 or f32 (y_dtype), rows y_stride >= n_out apart */
+int lora_linear(const lora_weights* w, const uint16_t* x, int64_t x_stride, int32_t T,
+                const int32_t* adapter_of, const void* base, int64_t base_stride, void* y,
+                int64_t y_stride, int32_t y_dtype, uint32_t* status, void* ws, size_t ws_bytes,
+                void* stream);
+
+/* The residual's addition and the root-mean-square norm, with the quantisation that
+ * the experts and the FP8 linears take:
+ *   r = x + residual, rounded to the residual's type (what res_out holds; without a
+ *       residual r = x),  y = r / sqrt(mean(r^2) + eps) * weight  in fp32
+ *   x [T][H] bf16, rows x_stride apart (a multiple of 8)
+ *   residual [T][H] bf16 or f32 (res_dtype), rows res_stride apart (a multiple of 8),
+ *     or NULL (res_out then NULL too)
+ *   weight [H] bf16 or NULL (1); eps >= 2^-100
+ *   res_out [T][H] of res_dtype, rows res_stride apart, or NULL; may be `residual`
+ *   y [T][H] bf16, contiguous, or NULL
+ *   q [T][H] u8 and scales [T][H/128] f32, contiguous: y quantised from fp32 by the
+ *     rule of act_quant_fp8 (not from the rounded y; NaN and infinities as
+ *     kv_append_rope has them in an E4M3 cache), or both NULL; H then a multiple
+ *     of 128
+ * One of y and q at least.  H is a multiple of 8 up to 16384.  Outputs overlap no input
+ * but as stated.  Sums of squares past fp32's range are formed again in units of a
+ * power of two; a row with a NaN or an infinity follows the formula. */
+int add_rmsnorm(const uint16_t* x, int64_t x_stride, const void* residual, int32_t res_dtype,
+                int64_t res_stride, int32_t T, int32_t H, const uint16_t* weight, float eps,
+                void* res_out, uint16_t* y, uint8_t* q, float* scales, void* stream);
+
 /* A paged key/value cache.  k and v are [n_pages][n_kv_heads][page_size]
  * [head_dim], bf16 or E4M3; an E4M3 cache has one fp32 scale per row in k_scale
  * and v_scale, [n_pages][n_kv_heads][page_size] (NULL for bf16).  page_size is
@@ -433,6 +495,56 @@ int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_strid
                        const int32_t* prefix_pages, int32_t prefix_len, const int32_t* page_table,
                        int32_t table_cols, int32_t max_keys, float scale, uint16_t* out,
                        float* lse, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/* Rules on the logits of T rows; what is NULL (n_bias 0) is left out.
+ *   history [n_seqs][>= max_history] int32, rows history_stride apart: token ids; row
+ *     t's text is the first n_tokens[t] of row seq_of[t] (NULL: row t; negative: no
+ *     text), and its first n_prompt[t] (NULL: 0) were given, the others
+ *     generated.  n_tokens is at most max_history (a longer text is cut, and sets
+ *     MOE_STATUS_BAD_INDEX, as does a seq_of >= n_seqs, which has no text).
+ *     Negative ids are padding; so is an id >= V, which sets MOE_STATUS_BAD_TOKEN.
+ *   repetition [T]: ids of the text: z > 0 ? z / repetition : z * repetition
+ *   presence, frequency [T]: ids generated c > 0 times: z - (presence + frequency c)
+ *   bias_ids [T][n_bias] int32, bias [T][n_bias] f32: added to z.  Of several entries of
+ *     one id the last counts; negative ids are no entry; so is an id >= V, which
+ *     sets MOE_STATUS_BAD_TOKEN
+ *   mask [n_masks] rows of ceil(V/32) words, mask_stride words apart: bit v % 32 of word
+ *     v / 32 allows id v; row t has mask mask_of[t] (NULL: mask t; negative: all
+ *     are allowed; so for a number >= n_masks, which sets MOE_STATUS_BAD_INDEX)
+ * The rule pointers are device memory, 4-byte aligned; the struct is host memory,
+ * read during the call only.  max_history < 2^20, n_bias <= 2047 (MOE_ENOTSUP beyond). */
+typedef struct logits_rules {
+  const int32_t* history;
+  int64_t history_stride;
+  int32_t max_history;
+  int32_t n_seqs;
+  const int32_t* seq_of;
+  const int32_t* n_tokens;
+  const int32_t* n_prompt;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const int32_t* bias_ids;
+  const float* bias;
+  const uint32_t* mask;
+  int64_t mask_stride;
+  const int32_t* mask_of;
+  int32_t n_masks;
+  int32_t n_bias;
+} logits_rules;
+
+/* out[t] = the logits z[t] under the rules, in this order: bias, repetition, presence
+ * and frequency, mask (-inf where an id is not allowed, whatever z is there).
+ * In fp32, rounded once.  A mask may leave a row nothing: it is then -inf
+ * throughout.
+ *   z [T][V] bf16 or f32, rows z_stride >= V apart
+ *   out [T][V] bf16 or f32, rows out_stride >= V apart; may be z, with z's type and
+ *     stride (logits that no rule touches are then not written); otherwise they
+ *     must not overlap
+ * z and out need the alignment of their elements only.  1 <= V <= 2^24. */
+int logits_adjust(const logits_rules* rules, const void* z, int32_t z_dtype, int64_t z_stride,
+                  int32_t T, int32_t V, void* out, int32_t out_dtype, int64_t out_stride,
+                  uint32_t* status, void* stream);
 
 /* Workspace bytes of token_logprobs (0 on invalid arguments). */
 size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top);

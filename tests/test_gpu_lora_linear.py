@@ -1,0 +1,218 @@
+"""lora_linear against 64 bits: every rank and split of its kernels, mixed adapters in a tile, tokens
+without one, what lies past a rank, NaN and infinities of other tokens and adapters."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import bit_expert_ffn_moe_amd as moe  # noqa: E402
+
+DEV = "cuda:0"
+
+
+def run(x, a, b, rank, scale, of, base, out, xs=None, ys=None, bs=None, in_place=False, stream=None):
+    """x [T][stride] etc. on the CPU; returns y [T][N] (CPU) and the status."""
+    T, (n, R, K), N = x.shape[0], a.shape, b.shape[1]
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    up = lambda t: t.to(DEV).contiguous() if t is not None else None  # noqa: E731
+    xd, ad, bd, rd, sd, od = (up(t) for t in (x, a, b, rank, scale, of))
+    based = up(base)
+    ys = ys or N
+    y = based if in_place else torch.full((T, ys), 5.0, dtype=dt, device=DEV)
+    bs = base.shape[1] if base is not None else 0
+    w = moe.make_lora(n, R, K, N, ad, bd, rd, sd)
+    nb = moe.lora_workspace_bytes(w, T)
+    assert nb > 0
+    ws = torch.full((nb // 4,), float("nan"), device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    moe.lora_linear(w, xd, x.shape[1], T, od, based, bs, y, bs if in_place else ys,
+                    moe.MOE_DT_BF16 if out == "bf16" else moe.MOE_DT_F32, st, ws, nb, stream)
+    torch.cuda.synchronize()
+    if not in_place and ys > N:
+        assert bool((y[:, N:] == 5).all())
+    return y.cpu()[:, :N], int(st.item())
+
+
+def expect(x, a, b, rank, scale, of, base, K):
+    """y and the size of what it is summed from, in 64 bits."""
+    T, n, R, N = x.shape[0], a.shape[0], a.shape[1], b.shape[1]
+    y = base[:, :N].double().clone() if base is not None else torch.zeros((T, N), dtype=torch.float64)
+    mag = torch.zeros((T, N), dtype=torch.float64)
+    for i in range(n):
+        t = torch.nonzero(of == i)[:, 0]
+        if not len(t):
+            continue
+        r = max(0, min(int(rank[i]), R)) if rank is not None else R
+        s = float(scale[i]) if scale is not None else 1.0
+        xd, ad, bd = x[t, :K].double(), a[i, :r].double(), b[i, :, :r].double()
+        y[t] += (xd @ ad.T) @ bd.T * s
+        mag[t] = (xd.abs() @ ad.abs().T) @ bd.abs().T * abs(s)
+    return y, mag
+
+
+def check(x, a, b, rank, scale, of, base, out, status=0, **kw):
+    K = a.shape[2]
+    y, st = run(x, a, b, rank, scale, of, base, out, **kw)
+    assert st == status
+    e, mag = expect(x, a, b, rank, scale, of, base, K)
+    # sums of K products, then of R, in fp32 (the matrix cores' additions within 2^-23 each), joined
+    # over 8 waves and 16 parts; then one rounding of y
+    tol = (K + a.shape[1] + 32) * 2.0 ** -23 * mag + (2.0 ** -8 if out == "bf16" else 2.0 ** -23) * e.abs()
+    bad = ~((y.double() - e).abs() <= tol + 1e-30)
+    assert not bool(bad.any()), (int(bad.sum()), float((y.double() - e).abs().max()))
+    return y
+
+
+def make(rng, T, K, N, n, R, out, ranks=False, pad=0, basis=True):
+    f = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32))  # noqa: E731
+    x, a, b = f(T, K + pad).to(torch.bfloat16), f(n, R, K).to(torch.bfloat16), f(n, N, R).to(torch.bfloat16)
+    rank = torch.from_numpy(rng.integers(0, R + 1, n).astype(np.int32)) if ranks else None
+    scale = torch.from_numpy((0.2 + rng.random(n)).astype(np.float32))
+    of = torch.from_numpy(rng.integers(-1, n, T).astype(np.int32))
+    base = (10 * f(T, N + pad)).to(torch.bfloat16 if out == "bf16" else torch.float32) if basis else None
+    return x, a, b, rank, scale, of, base
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 96, 128])
+def test_ranks(R, out):
+    rng = np.random.default_rng(R)
+    for T, K, N, n, ranks in [(1, 64, 64, 1, False), (1, 520, 100, 3, True), (16, 256, 1000, 5, True),
+                              (37, 1000, 65, 40, True), (5, 8, 1, 2, False)]:
+        print(R, out, T, K, N, n, flush=True)
+        check(*make(rng, T, K, N, n, R, out, ranks), out)
+
+
+@pytest.mark.parametrize("T,K,N,n,R", [(1, 4096, 300, 2, 16), (32, 2056, 500, 32, 64), (300, 600, 128, 6, 32),
+                                       (1500, 264, 70, 3, 8), (4100, 72, 40, 9, 16), (3, 70000, 17, 3, 8)])
+def test_sizes(T, K, N, n, R):
+    """The splits of x's columns: 1 to 8 steps a wave, several parts, several passes a part (70000)."""
+    rng = np.random.default_rng(T)
+    x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, "bf16", True, pad=8)
+    check(x, a, b, rank, scale, of, base, "bf16", ys=N + 3)
+    of = torch.from_numpy((np.arange(T) * n // T).astype(np.int32))      # runs of one adapter
+    check(x, a, b, rank, scale, of, base, "bf16", in_place=True)
+
+
+@pytest.mark.parametrize("R", [8, 16, 64])
+def test_exact_sums_keep_every_bit(R):
+    """Whole numbers whose sums stay below 2^24: fp32 outputs are exact, so nothing of a x is lost on
+    its way through the second product."""
+    rng = np.random.default_rng(R)
+    T, K, N, n = 19, 640, 130, 4
+    i = lambda lo, hi, *s: torch.from_numpy(rng.integers(lo, hi + 1, s).astype(np.float32))  # noqa: E731
+    x, a, b = i(-9, 9, T, K), i(-9, 9, n, R, K), i(-3, 3, n, N, R)
+    of = torch.from_numpy(rng.integers(-1, n, T).astype(np.int32))
+    base = i(-1000, 1000, T, N)
+    scale = torch.tensor([1.0, 2.0, 0.5, 4.0])
+    y, st = run(x.to(torch.bfloat16), a.to(torch.bfloat16), b.to(torch.bfloat16), None, scale, of, base, "f32")
+    e, mag = expect(x, a, b, None, scale, of, base, K)
+    hm = max(float((x[t].double() @ a[int(of[t])].double().T).abs().max()) for t in range(T) if of[t] >= 0)
+    assert hm > 2 ** 9 and float(mag.max()) < 2 ** 24      # more bits than a bf16 has, no sum is rounded
+    assert st == 0 and torch.equal(y.double(), e)
+
+
+def test_what_is_not_the_tokens_does_not_reach_it():
+    """NaN and infinities in other adapters, past the ranks, in other tokens of the tile; NaN between
+    the rows of x."""
+    rng = np.random.default_rng(1)
+    T, K, N, n, R = 20, 136, 90, 5, 32
+    x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, "f32", pad=8)
+    rank = torch.tensor([32, 7, 0, 17, 25], dtype=torch.int32)
+    of = torch.from_numpy(np.tile(np.array([0, 1, 2, 3, -1], np.int32), 4))
+    want = check(x, a, b, rank, scale, of, base, "f32")
+    for i in range(n):
+        r = int(rank[i])
+        a[i, r:], b[i, :, r:] = float("nan"), float("inf")
+    a[4], b[4], x[:, K:] = float("nan"), float("nan"), float("nan")
+    scale[4] = float("nan")
+    assert torch.equal(run(x, a, b, rank, scale, of, base, "f32")[0], want)
+    x[0], x[6, 3], x[4] = float("nan"), float("inf"), float("nan")       # tokens of adapters 0, 1, none
+    y, _ = run(x, a, b, rank, scale, of, base, "f32")
+    same = torch.ones(T, dtype=torch.bool)
+    same[0] = same[6] = False
+    assert torch.equal(y[same], want[same])
+    assert bool(y[0].isnan().all()) and not bool(y[6].isfinite().any())
+
+
+def test_no_base_no_adapter_and_bad_numbers():
+    rng = np.random.default_rng(2)
+    T, K, N, n, R = 18, 64, 77, 3, 16
+    x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, "bf16")
+    check(x, a, b, None, None, of, None, "bf16")
+    of[:] = -1
+    y, st = run(x, a, b, None, None, of, base, "bf16")
+    assert st == 0 and torch.equal(y, base)
+    y, st = run(x, a, b, None, None, of, None, "bf16")
+    assert st == 0 and bool((y == 0).all())
+    of[3], of[17], of[4] = n, 2 ** 31 - 1, 1
+    ok = of.clone()
+    ok[3] = ok[17] = -1
+    y, st = run(x, a, b, None, None, of, base, "bf16")
+    assert st == moe.MOE_STATUS_BAD_INDEX
+    assert torch.equal(y, run(x, a, b, None, None, ok, base, "bf16")[0])
+
+
+def test_in_place_leaves_other_rows_alone():
+    """Rows without an adapter are not written in place; rows behind the last token neither."""
+    rng = np.random.default_rng(3)
+    T, K, N, n, R = 21, 128, 96, 2, 8
+    x, a, b, _, scale, of, base = make(rng, T, K, N, n, R, "f32")
+    of[5] = -1
+    base[5, 7] = float("nan")
+    y = torch.cat([base, torch.full((3, N), 5.0)]).to(DEV)
+    w = moe.make_lora(n, R, K, N, a.to(DEV), b.to(DEV), None, scale.to(DEV))
+    nb = moe.lora_workspace_bytes(w, T)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    moe.lora_linear(w, x.to(DEV), K, T, of.to(DEV), y, N, y, N, moe.MOE_DT_F32, None, ws, nb)
+    torch.cuda.synchronize()
+    assert torch.equal(y[5].view(torch.int32).cpu(), base[5].view(torch.int32)) and bool((y[T:] == 5).all())
+
+
+def test_stacks_past_4_gib():
+    """Offsets past 32 bits in both stacks: the last of many adapters."""
+    K, N, R = 8192, 8192, 64
+    n = (1 << 32) // (R * K * 2) + 2
+    a = torch.zeros((n, R, K), dtype=torch.bfloat16, device=DEV)
+    b = torch.zeros((n, N, R), dtype=torch.bfloat16, device=DEV)
+    a[-1, :, -1], b[-1, -1, :] = 1.0, 2.0
+    x = torch.ones((1, K), dtype=torch.bfloat16, device=DEV)
+    of = torch.tensor([n - 1], dtype=torch.int32, device=DEV)
+    y = torch.empty((1, N), device=DEV)
+    w = moe.make_lora(n, R, K, N, a, b)
+    nb = moe.lora_workspace_bytes(w, 1)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    moe.lora_linear(w, x, K, 1, of, None, 0, y, N, moe.MOE_DT_F32, None, ws, nb)
+    torch.cuda.synchronize()
+    assert float(y[0, -1]) == 128.0 and float(y[0, :-1].abs().max()) == 0.0
+
+
+def test_captured_beside_eager_calls_with_a_workspace_each():
+    rng = np.random.default_rng(4)
+    T, K, N, n, R = 40, 512, 300, 6, 32
+    x, a, b, _, scale, of, base = (t.to(DEV) if t is not None else None for t in make(rng, T, K, N, n, R, "bf16"))
+    w = moe.make_lora(n, R, K, N, a, b, None, scale)
+    nb = moe.lora_workspace_bytes(w, T)
+    ws = [torch.empty(nb, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    out = [torch.empty((T, N), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+
+    def go(k):
+        moe.lora_linear(w, x, K, T, of, base, N, out[k], N, moe.MOE_DT_BF16, None, ws[k], nb)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        go(0)
+    for i in range(3):
+        x.copy_(torch.randn_like(x))
+        of.copy_(torch.randint(-1, n, (T,), dtype=torch.int32))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            go(1)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], out[1])
