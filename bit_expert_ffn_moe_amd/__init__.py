@@ -20,7 +20,7 @@ _SO = os.path.join(_PKG, "libbefmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_ENOTSUP, MOE_EALIGN, MOE_EWORKSPACE, MOE_ELAUNCH = 0, -1, -2, -3, -4, -5
 MOE_W_FP4_E2M1_UE8M0_K32, MOE_W_FP8_E4M3_F32_B128, MOE_W_INT4_BF16_GROUP = 1, 2, 3
-MOE_DT_BF16, MOE_DT_F32, MOE_DT_FP8_E4M3 = 1, 2, 3
+MOE_DT_BF16, MOE_DT_F32, MOE_DT_FP8_E4M3, MOE_DT_FP4_E2M1 = 1, 2, 3, 4
 MOE_STATUS_BAD_EXPERT_ID, MOE_STATUS_SYNC_TIMEOUT = 1, 2
 MOE_STATUS_BAD_PAGE, MOE_STATUS_BAD_TOKEN, MOE_STATUS_BAD_INDEX = 4, 8, 16
 ROPE_HALF = MOE_ROPE_HALF = 1

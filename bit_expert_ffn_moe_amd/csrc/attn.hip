@@ -60,6 +60,20 @@ __device__ __forceinline__ uint4 fp8x8(uint32_t a, uint32_t b) {
   return make_uint4(fp8_lo(a), fp8_hi(a), fp8_lo(b), fp8_hi(b));
 }
 
+// The scale operand of UE8M0 byte b (only the exponent field counts): 2^(b - 127), or NaN
+// above 252, where 6 times it is past bf16.
+__device__ __forceinline__ float fp4_scale(uint32_t b) {
+  return __uint_as_float(b > 252u ? 0x7fc00000u : b << 23);
+}
+// eight E2M1 codes -> four dwords of bf16 pairs (exact: two significant bits)
+__device__ __forceinline__ uint4 fp4x8(uint32_t v, float sc) {
+  return make_uint4(
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, sc, 0)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, sc, 1)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, sc, 2)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, sc, 3)));
+}
+
 // W consecutive dwords (1, 2, 4 or 8) at an address aligned to min(4 W, 16).
 template <int W>
 __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&d)[W]) {
@@ -209,21 +223,24 @@ __device__ __forceinline__ bool bad_key(const AttnArgs& a, const int32_t* pages,
 // A tile's K is dead once the scores are formed and its V once they are
 // multiplied, so the next tile's are loaded into the same registers right
 // then: a load has the rest of a tile's work to arrive in.
-template <int D, bool FP8, int RT>
+template <int D, int KV, int RT>
 __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int r0, int rows,
                                           const Range& rg, int part, float* lds) {
   constexpr int NS = D / 32;        // 32-column steps of the score product
   constexpr int VD = D / 16;        // columns per lane of V and O
-  constexpr int ES = FP8 ? 1 : 2;
-  constexpr int NK = FP8 ? NS / 2 : NS;      // 16-byte K loads per 16 keys
-  constexpr int VW = VD * ES / 4;            // dwords per key of this lane's V columns
+  constexpr bool FP8 = KV == kKvE4M3, FP4 = KV == kKvE2M1;
+  constexpr int RB = FP4 ? D / 2 : FP8 ? D : 2 * D;  // bytes of a cache row
+  constexpr int NK = FP8 ? NS / 2 : NS;      // 16-byte K loads per 16 keys (bf16, E4M3)
+  constexpr int VW = VD * (FP8 ? 1 : 2) / 4; // dwords per key of this lane's V columns (E2M1: as bf16)
+  constexpr int SB = D / 32;                 // E2M1: scale bytes of a row
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int slots = (1 << a.page_shift) - 1;
 
   // this lane's query of each row tile, its operand and its limit.  Column order of
   // the score product: bf16 K, step s of group g holds columns 32 s + 8 g; FP8 K,
-  // steps 2u and 2u+1 the halves of the 16 codes from 64 u + 16 g
+  // steps 2u and 2u+1 the halves of the 16 codes from 64 u + 16 g; E2M1 K, columns 8 s
+  // of the g-th quarter of the row
   auto row_of = [&](int rt, int& tok, int& head) {
     const int rr = min(r0 + 16 * rt + c, rows - 1);
     tok = t0 + rr / a.G;
@@ -243,7 +260,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
 #pragma unroll
     for (int s = 0; s < NS; ++s)
       q[rt][s] = *reinterpret_cast<const uint4*>(
-          qr + (FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g));
+          qr + (FP4 ? D / 4 * g + 8 * s : FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g));
   }
   maxlim = __builtin_amdgcn_readfirstlane(wave_max_all(maxlim));
   minlim = __builtin_amdgcn_readfirstlane(wave_min_all(minlim));
@@ -279,26 +296,80 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     }
     return r;
   };
-  const uint32_t ko = (c * D + (FP8 ? 16 : 8) * g) * ES, vo = (4 * g * D + VD * c) * ES;
+  const uint32_t ko = c * RB + (FP4 ? D / 8 : 16) * g, vo = 4 * g * RB + RB / 16 * c;
   uint4 kr[2][NK];
   float4 ks4[2], vs4[2];
   uint32_t vr[8][VW];
+  // E2M1: a quarter of a K row with its scale bytes (one, or two at 256 columns; at 64
+  // two groups share one); a lane's V columns of 8 keys as loaded, and the scale bytes of
+  // all columns of these keys
+  constexpr int KW = D / 32, VSW = D / 32;
+  uint32_t kq[2][KW], ksb[2], vq[8][D == 256 ? 2 : 1], vsb[2][VSW];
   auto load_k = [&](const Rows& r) {
+    if constexpr (FP4) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        load_dwords((const uint8_t*)a.k + r.row[u] * RB + ko, kq[u]);
+        const uint8_t* sb = (const uint8_t*)a.ks + r.row[u] * SB;
+        if constexpr (D == 256)
+          ksb[u] = *reinterpret_cast<const uint16_t*>(sb + c * SB + 2 * g);
+        else
+          ksb[u] = sb[c * SB + (D == 64 ? g >> 1 : g)];
+      }
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint8_t* kb = (const uint8_t*)a.k + r.row[u] * (D * ES);
+      const uint8_t* kb = (const uint8_t*)a.k + r.row[u] * RB;
 #pragma unroll
       for (int s = 0; s < NK; ++s) kr[u][s] = *reinterpret_cast<const uint4*>(kb + ko + 64 * s);
       if constexpr (FP8) {
-        ks4[u] = *reinterpret_cast<const float4*>(a.ks + r.row[u] + 4 * g);
-        vs4[u] = *reinterpret_cast<const float4*>(a.vs + r.row[u] + 4 * g);
+        ks4[u] = *reinterpret_cast<const float4*>((const float*)a.ks + r.row[u] + 4 * g);
+        vs4[u] = *reinterpret_cast<const float4*>((const float*)a.vs + r.row[u] + 4 * g);
       }
     }
   };
   auto load_v = [&](const Rows& r) {
+    if constexpr (FP4) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t* vb = (const uint8_t*)a.v + r.row[e >> 2] * RB + vo + (e & 3) * RB;
+        if constexpr (D == 64)
+          vq[e][0] = *reinterpret_cast<const uint16_t*>(vb);
+        else
+          load_dwords(vb, vq[e]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        load_dwords((const uint8_t*)a.vs + (r.row[u] + 4 * g) * SB, vsb[u]);
+      return;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      load_dwords((const uint8_t*)a.v + r.row[e >> 2] * (D * ES) + vo + (e & 3) * (D * ES), vr[e]);
+      load_dwords((const uint8_t*)a.v + r.row[e >> 2] * RB + vo + (e & 3) * RB, vr[e]);
+  };
+  // E2M1 V as bf16, from here on as if loaded so
+  auto widen_v = [&] {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // byte VD c / 32 of the row's scale bytes, which are half a dword, one or two
+      const uint32_t w = D == 64    ? vsb[e >> 2][(e & 3) >> 1] >> 16 * (e & 1)
+                         : D == 128 ? vsb[e >> 2][e & 3]
+                         : c < 8    ? vsb[e >> 2][(2 * (e & 3)) % VSW]
+                                    : vsb[e >> 2][(2 * (e & 3) + 1) % VSW];
+      const float sc = fp4_scale(w >> 8 * (VD * c / 32 & 3) & 0xffu);
+      if constexpr (D == 64) {
+        const uint4 x = fp4x8(vq[e][0], sc);
+        vr[e][0] = x.x, vr[e][1 % VW] = x.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < VW; i += 4) {
+          const uint4 x = fp4x8(vq[e][i / 4], sc);
+          vr[e][i] = x.x, vr[e][(i + 1) % VW] = x.y, vr[e][(i + 2) % VW] = x.z,
+          vr[e][(i + 3) % VW] = x.w;
+        }
+      }
+    }
   };
 
   // V rows that no row of the item sees may hold anything: cleared.  A
@@ -339,6 +410,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     auto key_of = [&](int e) { return j0 + 16 * (e >> 2) + 4 * g + (e & 3); };
     auto inside = [&](int e) { return key_of(e) >= lo && key_of(e) < hi && !cur.bad[e >> 2]; };
 
+    if constexpr (FP4 && !SLOW) widen_v();  // (SLOW: widened and cleared before)
     if (!SLOW && edge && leaks(j0, cur)) {
       after_k();
       after_v();
@@ -353,7 +425,9 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          if constexpr (FP8) {
+          if constexpr (FP4) {
+            kf[u][s] = fp4x8(kq[u][s], fp4_scale(D == 256 ? ksb[u] >> 8 * (s >> 2) & 0xffu : ksb[u]));
+          } else if constexpr (FP8) {
             const uint4 k = kr[u][s / 2];
             kf[u][s] = (s & 1) ? fp8x8(k.z, k.w) : fp8x8(k.x, k.y);
           } else {
@@ -531,6 +605,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
       if (!(j0 < lo || j0 + 32 > min(hi, minlim) || cur.bad[0] || cur.bad[1])) continue;
       load_k(cur);
       load_v(cur);
+      if constexpr (FP4) widen_v();
       if (leaks(j0, cur)) tile(std::true_type{}, j0, cur, [] {}, [] {});
     }
   }
@@ -651,16 +726,16 @@ __device__ __forceinline__ bool item_of(const AttnArgs& a, int item, int np, Ite
 }
 
 // RTP, RTS: row tiles of a block of the prefix's and of the sequences' own items.
-template <int D, bool FP8, int RTP, int RTS>
+template <int D, int KV, int RTP, int RTS>
 __global__ __launch_bounds__(256, D < 256 && RTP == 1 ? 3 : 2) void attn_part_kernel(AttnArgs a,
                                                                                     int np) {
   __shared__ __align__(8) float lds[4 * 64 * 2 + 2 * (D / 16) * 4 * 64];
   Item it;
   if (!item_of(a, blockIdx.x, np, it)) return;
   if (RTP == RTS || (int)blockIdx.x < np)
-    attn_item<D, FP8, RTP>(a, it.h, it.t0, it.rb * 16 * RTP, it.rows, it.rg, it.part, lds);
+    attn_item<D, KV, RTP>(a, it.h, it.t0, it.rb * 16 * RTP, it.rows, it.rg, it.part, lds);
   else
-    attn_item<D, FP8, RTS>(a, it.h, it.t0, it.rb * 16 * RTS, it.rows, it.rg, it.part, lds);
+    attn_item<D, KV, RTS>(a, it.h, it.t0, it.rb * 16 * RTS, it.rows, it.rg, it.part, lds);
 }
 
 // ---- many rows: keys staged in LDS for eight waves of rows -------------------
@@ -677,10 +752,14 @@ __global__ __launch_bounds__(256, D < 256 && RTP == 1 ? 3 : 2) void attn_part_ke
 // matrix cores busy for 27% of that.  (Forming the scores of the next 32 keys
 // under the exponentials of these takes the registers that hide LDS and loads: 170
 // us bf16.)
-template <int D, bool FP8, int RT>
+template <int D, int KV, int RT>
 __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
-  constexpr int NS = D / 32, VD = D / 16, ES = FP8 ? 1 : 2;
-  constexpr int KC = D * ES / 16;                 // 16-byte pieces of a K row
+  constexpr int NS = D / 32, VD = D / 16;
+  constexpr bool FP8 = KV == kKvE4M3, FP4 = KV == kKvE2M1;
+  constexpr int RB = FP4 ? D / 2 : FP8 ? D : 2 * D;  // bytes of a cache row
+  constexpr int KC = RB / 16;                     // 16-byte pieces of a K row
+  constexpr int SB = D / 32;                      // E2M1: scale bytes of a row, one per piece
+  constexpr int VRW = FP4 ? 1 : FP8 ? 2 : 4;      // dwords of a V unit's key
   constexpr int NKL = 64 * KC / 512 ? 64 * KC / 512 : 1;   // K pieces per thread
   constexpr int CH = D / 8;                       // 16-byte chunks of an LDS K row
   __shared__ uint4 lk[2][64][CH];
@@ -743,7 +822,8 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
   constexpr int NV = 32 / VPR ? 32 / VPR : 1;
   static_assert(NV * VPR >= 32, "V rounds");
   uint4 kreg[NKL];
-  uint32_t vreg[NV][2][FP8 ? 2 : 4];
+  uint32_t vreg[NV][2][VRW];
+  uint8_t ksb[NKL], vsb[NV][2];  // E2M1: their scales
   float sreg = 0.0f;
   const int32_t* pages = itm.rg.pages;
   // the pages of this thread's pieces, fetched a tile ahead of them (a V unit's
@@ -776,7 +856,8 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
       if (64 * KC >= 512 || tid < 64 * KC) {
         bool ok;
         const size_t row = row_at(j0 + kkey + KPR * i, pgk[i], ok);
-        kreg[i] = *reinterpret_cast<const uint4*>((const uint8_t*)a.k + row * (D * ES) + 16 * kpc);
+        kreg[i] = *reinterpret_cast<const uint4*>((const uint8_t*)a.k + row * RB + 16 * kpc);
+        if constexpr (FP4) ksb[i] = ((const uint8_t*)a.ks)[row * SB + kpc];
       }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -785,14 +866,15 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
         for (int k = 0; k < 2; ++k) {
           bool ok;
           const size_t row = row_at(j0 + 2 * (vkp0 + VPR * i) + k, pgv[i], ok);
-          load_dwords((const uint8_t*)a.v + row * (D * ES) + 8 * ES * vcol, vreg[i][k]);
+          load_dwords((const uint8_t*)a.v + row * RB + 4 * VRW * vcol, vreg[i][k]);
+          if constexpr (FP4) vsb[i][k] = ((const uint8_t*)a.vs)[row * SB + (vcol >> 2)];
           okbits |= ok ? 1u << (2 * i + k) : 0u;
         }
       }
     if (FP8 && tid < 128) {
       bool ok;
       const size_t row = row_at(j0 + (tid & 63), pgs, ok);
-      sreg = (tid < 64 ? a.ks : a.vs)[row];
+      sreg = ((const float*)(tid < 64 ? a.ks : a.vs))[row];
       okbits |= ok ? 0x80000000u : 0u;
     }
   };
@@ -804,7 +886,13 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
       if (64 * KC >= 512 || tid < 64 * KC) {
         const int r = kkey + KPR * i;
         const uint4 x = kreg[i];
-        if constexpr (FP8) {
+        if constexpr (FP4) {
+          const float sc = fp4_scale(ksb[i]);
+          lk[buf][r][swz_k(r, 4 * kpc)] = fp4x8(x.x, sc);
+          lk[buf][r][swz_k(r, 4 * kpc + 1)] = fp4x8(x.y, sc);
+          lk[buf][r][swz_k(r, 4 * kpc + 2)] = fp4x8(x.z, sc);
+          lk[buf][r][swz_k(r, 4 * kpc + 3)] = fp4x8(x.w, sc);
+        } else if constexpr (FP8) {
           lk[buf][r][swz_k(r, 2 * kpc)] = fp8x8(x.x, x.y);
           lk[buf][r][swz_k(r, 2 * kpc + 1)] = fp8x8(x.z, x.w);
         } else {
@@ -816,17 +904,29 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
     for (int i = 0; i < NV; ++i)
       if (VPR <= 32 || vkp0 < 32) {
         const int kp = vkp0 + VPR * i;
+        constexpr int W = FP8 ? 2 : 4;
+        uint32_t vx[2][W];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (FP4) {
+            const uint4 x = fp4x8(vreg[i][k][0], fp4_scale(vsb[i][k]));
+            vx[k][0] = x.x, vx[k][1] = x.y, vx[k][2 % W] = x.z, vx[k][3 % W] = x.w;
+          } else {
+#pragma unroll
+            for (int w = 0; w < W; ++w) vx[k][w] = vreg[i][k][w % VRW];
+          }
+        }
         // rows outside the item's keys may hold anything: cleared
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (!(okbits >> (2 * i + k) & 1u))
 #pragma unroll
-            for (int w = 0; w < (FP8 ? 2 : 4); ++w) vreg[i][k][w] = 0u;
+            for (int w = 0; w < W; ++w) vx[k][w] = 0u;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int w = 0; w < (FP8 ? 2 : 4); ++w) {
-            const uint32_t x = vreg[i][k][w];
+          for (int w = 0; w < W; ++w) {
+            const uint32_t x = vx[k][w];
             if (FP8)
               leak |= (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
             else
@@ -840,10 +940,10 @@ __global__ __launch_bounds__(512, 2) void attn_tile_kernel(AttnArgs a, int np) {
           uint32_t two;
           if constexpr (FP8)
             two = __builtin_bit_cast(
-                uint32_t, e4m3x2_lo(__builtin_amdgcn_perm(vreg[i][1][e / 4], vreg[i][0][e / 4],
+                uint32_t, e4m3x2_lo(__builtin_amdgcn_perm(vx[1][e / 4], vx[0][e / 4],
                                                           0x0c0c0400u + 0x0101u * (e & 3))));
           else
-            two = __builtin_amdgcn_perm(vreg[i][1][e / 2], vreg[i][0][e / 2],
+            two = __builtin_amdgcn_perm(vx[1][e / 2 % W], vx[0][e / 2 % W],
                                         (e & 1) ? 0x07060302u : 0x05040100u);
           const int d = 8 * vcol + e;
           reinterpret_cast<uint32_t*>(&lv[buf][d][swz_v(d, slot >> 3)])[(slot & 7) >> 1] = two;
@@ -1129,38 +1229,40 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 namespace {
 
 // Items whose blocks take few rows (AttnArgs kinds 1, 2), both sorts in one launch.
-template <int D, bool FP8>
+template <int D, int KV>
 void launch_few(const AttnArgs& a, int np, int no, hipStream_t st) {
   const bool p2 = np && a.prefix_kind == 2, s2 = no && a.own_kind == 2;
   if constexpr (D < 256) {
     if (p2 && !s2 && no) {
-      attn_part_kernel<D, FP8, 2, 1><<<np + no, 256, 0, st>>>(a, np);
+      attn_part_kernel<D, KV, 2, 1><<<np + no, 256, 0, st>>>(a, np);
       return;
     }
     if (p2 || s2) {  // (where both are there, the prefix's rows are the more)
-      attn_part_kernel<D, FP8, 2, 2><<<np + no, 256, 0, st>>>(a, np);
+      attn_part_kernel<D, KV, 2, 2><<<np + no, 256, 0, st>>>(a, np);
       return;
     }
   }
-  attn_part_kernel<D, FP8, 1, 1><<<np + no, 256, 0, st>>>(a, np);
+  attn_part_kernel<D, KV, 1, 1><<<np + no, 256, 0, st>>>(a, np);
 }
 
-template <int D, bool FP8>
+template <int D, int KV>
 void launch_dim(const AttnArgs& a, hipStream_t st) {
   const int np = a.n_prefix_parts * a.Hkv * a.prefix_blocks;
   const int no = a.n_own_parts * a.B * a.Hkv * a.own_blocks;
   constexpr int RT = D == 256 ? 1 : 2;
   const int tp = a.prefix_kind == kAttnTile ? np : 0, ts = a.own_kind == kAttnTile ? no : 0;
-  if (tp + ts) attn_tile_kernel<D, FP8, RT><<<tp + ts, 512, 0, st>>>(a, tp);
-  if (np + no > tp + ts) launch_few<D, FP8>(a, np - tp, no - ts, st);
+  if (tp + ts) attn_tile_kernel<D, KV, RT><<<tp + ts, 512, 0, st>>>(a, tp);
+  if (np + no > tp + ts) launch_few<D, KV>(a, np - tp, no - ts, st);
 }
 
 template <int D>
 void launch_all(const AttnArgs& a, hipStream_t st) {
-  if (a.fp8)
-    launch_dim<D, true>(a, st);
+  if (a.kv == kKvE2M1)
+    launch_dim<D, kKvE2M1>(a, st);
+  else if (a.kv == kKvE4M3)
+    launch_dim<D, kKvE4M3>(a, st);
   else
-    launch_dim<D, false>(a, st);
+    launch_dim<D, kKvBf16>(a, st);
   constexpr int RPB = 256 / (D / 4 * kJoinGroups);
   const int64_t rows = (int64_t)a.n_tok * a.Hq;
   const unsigned blocks = (unsigned)((rows + RPB - 1) / RPB);

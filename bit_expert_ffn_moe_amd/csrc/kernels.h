@@ -221,10 +221,13 @@ struct LogitsArgs {
 };
 hipError_t launch_logits(const LogitsArgs& a, hipStream_t st);
 
+// What a key/value cache holds: bf16, E4M3 with a scale a row, E2M1 with a scale per 32
+// columns.
+constexpr int kKvBf16 = 0, kKvE4M3 = 1, kKvE2M1 = 2;
+
 // Paged cache append with rotation (kv.hip).
 struct KvAppendArgs {
-  void *kc, *vc;
-  float *ks, *vs;
+  void *kc, *vc, *ks, *vs;
   const uint16_t *q, *k, *v;
   uint16_t* q_out;
   int64_t q_stride, k_stride, v_stride;
@@ -233,7 +236,8 @@ struct KvAppendArgs {
   uint32_t* status;
   int T, Hq, Hkv, D, R, rope_rows, n_seqs, table_cols, n_pages, page_shift;
   int iters;               // set by the launcher: head groups per block
-  bool fp8, pairs;
+  int kv;                  // kKv*
+  bool pairs;
 };
 hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st);
 
@@ -256,8 +260,7 @@ hipError_t launch_logprobs(const LogprobArgs& a, bool bf16, hipStream_t st);
 // Shared-prefix attention (attn.hip).
 constexpr int kAttnTile = 3;
 struct AttnArgs {
-  const void *k, *v;
-  const float *ks, *vs;
+  const void *k, *v, *ks, *vs;
   const uint16_t* q;
   int64_t q_stride;
   const int32_t *pos, *prefix_pages, *table;
@@ -269,7 +272,7 @@ struct AttnArgs {
   float scale_log2;             // scale * log2(e)
   int B, Q, n_tok, Hq, Hkv, G, D;
   int table_cols, n_pages, page_shift, prefix_len, max_keys;
-  bool fp8;
+  int kv;                       // kKv*
   // split of the prefix's items and of the sequences' own: kind (1, 2: blocks of
   // 16 x kind rows, keys straight to registers; kAttnTile: of 256 rows, 128 at 256
   // columns, keys through LDS), row blocks, keys per part, parts

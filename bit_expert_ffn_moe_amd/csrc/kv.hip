@@ -6,8 +6,8 @@
 // and the sum are rounded separately (no fused multiply-add), so the result is
 // the fp32 evaluation of the formula as written, bit for bit, whatever the
 // head layout.  K (rotated) and V go to the token's slot as bf16 (nearest
-// even), or as E4M3 codes with one fp32 scale amax/448 per (token, head) by
-// the act_quant rule.
+// even), as E4M3 codes with one fp32 scale amax/448 per (token, head) by
+// the act_quant rule, or as E2M1 codes with a power of two per 32 columns.
 //
 // HBM-bound elementwise work.  One lane owns 8 consecutive elements of a head
 // (16 bytes of bf16), D/8 lanes a head, so the pair partner of the "half"
@@ -26,6 +26,33 @@ namespace bef {
 
 namespace {
 
+// E2M1 codes (nearest even) of a lane's 8 values and the UE8M0 byte of the 32 columns that
+// it shares with the other three lanes of its quad: the smallest power of two that
+// brings their largest to 6 at most, so that no value is off by more than half the
+// step between its neighbours (with the power below, 6 to 8 times it would all become
+// 6).  Bytes end at 252: 6 times the next power is past bf16.  A NaN or an infinity
+// leaves the group no value: byte 255.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], uint32_t& sb) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    amax = fmaxf(amax, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : INFINITY);
+  const uint32_t top = __float_as_uint(group_max<4>(amax));
+  const int e = max(0, min((int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x400000u ? 1 : 0), 252));
+  float u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    u[i] = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(v[i], 127 - e), -6.0f, 6.0f);
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, u[0], u[1], 1.0f, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, u[2], u[3], 1.0f, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, u[4], u[5], 1.0f, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, u[6], u[7], 1.0f, 3);
+  const bool none = top == 0x7f800000u;
+  sb = none ? 255u : (uint32_t)e;
+  return none ? 0u : q;
+}
+
 // The rotated pair, each operation rounded on its own (the empty asm keeps the
 // products as values of their own: this library is compiled with fused
 // multiply-adds allowed everywhere).
@@ -40,7 +67,7 @@ __device__ __forceinline__ void rotate(float a, float b, float c, float s, float
 
 // grid: (tokens, head groups).  LPH lanes per head (D/8); a block of 256 takes
 // 256/LPH heads at a time, `iters` times.
-template <int LPH, bool FP8, bool PAIRS>
+template <int LPH, int KV, bool PAIRS>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
   constexpr int D = LPH * 8, HPB = 256 / LPH;
   const int t = blockIdx.x;
@@ -111,25 +138,30 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
     }
     const size_t row = (((size_t)page * a.Hkv + (is_v ? kvh - a.Hkv : kvh)) << a.page_shift) + slot;
     uint8_t* dst = (uint8_t*)(is_v ? a.vc : a.kc);
-    if (!FP8) {
+    if constexpr (KV == kKvBf16) {
       *reinterpret_cast<uint4*>(dst + (row * D + 8 * c) * 2) = pack8(v);
-    } else {
+    } else if constexpr (KV == kKvE4M3) {
       float sc;
       const uint2 q = e4m3x8<LPH>(v, sc);
       *reinterpret_cast<uint2*>(dst + row * D + 8 * c) = q;
-      if (c == 0) (is_v ? a.vs : a.ks)[row] = sc;
+      if (c == 0) ((float*)(is_v ? a.vs : a.ks))[row] = sc;
+    } else {
+      uint32_t sb;
+      const uint32_t q = e2m1x8(v, sb);
+      *reinterpret_cast<uint32_t*>(dst + row * (D / 2) + 4 * c) = q;
+      if ((c & 3) == 0) ((uint8_t*)(is_v ? a.vs : a.ks))[row * (D / 32) + (c >> 2)] = (uint8_t)sb;
     }
   }
 }
 
 namespace {
 
-template <int LPH, bool FP8>
+template <int LPH, int KV>
 void launch_style(const KvAppendArgs& a, dim3 grid, hipStream_t st) {
   if (a.pairs)
-    kv_append_kernel<LPH, FP8, true><<<grid, 256, 0, st>>>(a);
+    kv_append_kernel<LPH, KV, true><<<grid, 256, 0, st>>>(a);
   else
-    kv_append_kernel<LPH, FP8, false><<<grid, 256, 0, st>>>(a);
+    kv_append_kernel<LPH, KV, false><<<grid, 256, 0, st>>>(a);
 }
 
 template <int LPH>
@@ -142,10 +174,12 @@ void launch_dim(KvAppendArgs a, hipStream_t st) {
   // 5.4 the other way; 32 tokens: 3.4 and 4.3).
   a.iters = a.T >= 1024 ? groups : 1;
   const dim3 grid(a.T, (groups + a.iters - 1) / a.iters);
-  if (a.fp8)
-    launch_style<LPH, true>(a, grid, st);
+  if (a.kv == kKvE2M1)
+    launch_style<LPH, kKvE2M1>(a, grid, st);
+  else if (a.kv == kKvE4M3)
+    launch_style<LPH, kKvE4M3>(a, grid, st);
   else
-    launch_style<LPH, false>(a, grid, st);
+    launch_style<LPH, kKvBf16>(a, grid, st);
 }
 
 }  // namespace

@@ -19,17 +19,22 @@ int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }
 
 int check_cache(const kv_cache* c) {
   if (!c || !c->k || !c->v) return MOE_EINVAL;
-  if (c->dtype != MOE_DT_BF16 && c->dtype != MOE_DT_FP8_E4M3) return MOE_EINVAL;
+  if (c->dtype != MOE_DT_BF16 && c->dtype != MOE_DT_FP8_E4M3 && c->dtype != MOE_DT_FP4_E2M1)
+    return MOE_EINVAL;
   if (c->n_pages < 1 || c->n_kv_heads < 1 || c->page_size < 1) return MOE_EINVAL;
   if (c->page_size & (c->page_size - 1)) return MOE_EINVAL;
   if (c->page_size < 16 || c->page_size > 1024 || c->n_kv_heads > 1024) return MOE_ENOTSUP;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_ENOTSUP;
-  const bool fp8 = c->dtype == MOE_DT_FP8_E4M3;
-  if (fp8 != (c->k_scale != nullptr) || fp8 != (c->v_scale != nullptr)) return MOE_EINVAL;
+  const bool scaled = c->dtype != MOE_DT_BF16;
+  if (scaled != (c->k_scale != nullptr) || scaled != (c->v_scale != nullptr)) return MOE_EINVAL;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) ||
       !aligned(c->v_scale, 16))
     return MOE_EALIGN;
   return MOE_OK;
+}
+
+int kv_kind(const kv_cache* c) {
+  return c->dtype == MOE_DT_BF16 ? kKvBf16 : c->dtype == MOE_DT_FP8_E4M3 ? kKvE4M3 : kKvE2M1;
 }
 
 int log2_of(int v) {
@@ -96,7 +101,7 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   a->Hq = n_q_heads, a->Hkv = c->n_kv_heads, a->G = n_q_heads / c->n_kv_heads, a->D = c->head_dim;
   a->n_pages = c->n_pages, a->page_shift = log2_of(c->page_size);
   a->prefix_len = prefix_len, a->max_keys = max_keys;
-  a->fp8 = c->dtype == MOE_DT_FP8_E4M3;
+  a->kv = kv_kind(c);
   split_rows(a->n_tok * a->G, a->D, &a->prefix_kind, &a->prefix_blocks);
   split_rows(q_len * a->G, a->D, &a->own_kind, &a->own_blocks);
   const int base_p = a->Hkv * a->prefix_blocks;
@@ -354,14 +359,14 @@ int kv_append_rope(const kv_cache* cache, const uint16_t* q, int64_t q_stride, i
   if (rc) return rc;
   KvAppendArgs a;
   memset(&a, 0, sizeof a);
-  a.kc = cache->k, a.vc = cache->v, a.ks = (float*)cache->k_scale, a.vs = (float*)cache->v_scale;
+  a.kc = cache->k, a.vc = cache->v, a.ks = cache->k_scale, a.vs = cache->v_scale;
   a.q = q, a.k = k, a.v = v, a.q_out = q_out;
   a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
   a.rope = rope, a.seq_of = seq_of, a.pos = pos, a.table = page_table, a.status = status;
   a.T = T, a.Hq = n_q_heads, a.Hkv = cache->n_kv_heads, a.D = cache->head_dim, a.R = rope_dim;
   a.rope_rows = rope_rows, a.n_seqs = n_seqs, a.table_cols = table_cols;
   a.n_pages = cache->n_pages, a.page_shift = log2_of(cache->page_size);
-  a.fp8 = cache->dtype == MOE_DT_FP8_E4M3, a.pairs = rope_style == MOE_ROPE_PAIRS;
+  a.kv = kv_kind(cache), a.pairs = rope_style == MOE_ROPE_PAIRS;
   return launch_status(launch_kv_append(a, (hipStream_t)stream));
 }
 
@@ -396,7 +401,7 @@ int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_strid
   if (ws_bytes < attn_bytes(a)) return MOE_EWORKSPACE;
   rc = check_device();
   if (rc) return rc;
-  a.k = cache->k, a.v = cache->v, a.ks = (float*)cache->k_scale, a.vs = (float*)cache->v_scale;
+  a.k = cache->k, a.v = cache->v, a.ks = cache->k_scale, a.vs = cache->v_scale;
   a.q = q, a.q_stride = q_stride, a.pos = pos, a.prefix_pages = prefix_pages;
   a.table = page_table, a.table_cols = table_cols;
   a.out = out, a.lse = lse, a.status = status;

@@ -74,8 +74,9 @@ enum {
                                    zero point per group of inputs             */
 };
 
-/* Activation / output dtypes (MOE_DT_FP8_E4M3: key/value caches only). */
-enum { MOE_DT_BF16 = 1, MOE_DT_F32 = 2, MOE_DT_FP8_E4M3 = 3 };
+/* Activation / output dtypes (MOE_DT_FP8_E4M3, MOE_DT_FP4_E2M1: key/value
+ * caches only). */
+enum { MOE_DT_BF16 = 1, MOE_DT_F32 = 2, MOE_DT_FP8_E4M3 = 3, MOE_DT_FP4_E2M1 = 4 };
 
 /* Device status word bits (see moe_device_status).  MOE_STATUS_SYNC_TIMEOUT:
  * on the small-T router or the one-token path, a block waiting for the
@@ -410,10 +411,12 @@ int add_rmsnorm(const uint16_t* x, int64_t x_stride, const void* residual, int32
                 void* res_out, uint16_t* y, uint8_t* q, float* scales, void* stream);
 
 /* A paged key/value cache.  k and v are [n_pages][n_kv_heads][page_size]
- * [head_dim], bf16 or E4M3; an E4M3 cache has one fp32 scale per row in k_scale
- * and v_scale, [n_pages][n_kv_heads][page_size] (NULL for bf16).  page_size is
- * a power of two, 16 to 1024; head_dim 64, 128 or 256; n_kv_heads <= 1024.
- * The descriptor is host memory, read during the call only. */
+ * [head_dim], bf16, E4M3 or E2M1 (two codes per byte, element 2j in bits 0-3).  An E4M3
+ * cache has one fp32 scale per row in k_scale and v_scale, [n_pages][n_kv_heads]
+ * [page_size]; an E2M1 cache one UE8M0 byte per 32 columns, [n_pages][n_kv_heads]
+ * [page_size][head_dim/32], whose bytes above 252 stand for 32 NaN; NULL for bf16.
+ * page_size is a power of two, 16 to 1024; head_dim 64, 128 or 256; n_kv_heads
+ * <= 1024.  The descriptor is host memory, read during the call only. */
 typedef struct kv_cache {
   int32_t dtype;
   int32_t n_pages;
@@ -423,8 +426,8 @@ typedef struct kv_cache {
   int32_t pad_;
   void* k;
   void* v;
-  float* k_scale;
-  float* v_scale;
+  void* k_scale; /* float (E4M3) or uint8_t (E2M1) */
+  void* v_scale;
 } kv_cache;
 
 /* How pairs are laid out in a rotated head of rope_dim elements: element i
@@ -439,7 +442,10 @@ enum { MOE_ROPE_HALF = 1, MOE_ROPE_PAIRS = 2 };
  * the other elements and v are taken as they are.  Cache rows are bf16 (nearest
  * even), or E4M3 by the rule of act_quant_fp8 over the whole head row, where a NaN
  * becomes E4M3's NaN and leaves the row's other values as they are; an infinity
- * leaves the row no finite value (scale inf).
+ * leaves the row no finite value (scale inf).  In an E2M1 cache each 32 columns have
+ * the smallest power of two that brings their largest to 6 at most (2^-127 at least,
+ * 2^125 at most, where larger values become 6), and codes are rounded to nearest
+ * even; a NaN or an infinity makes the 32 columns NaN (byte 255).
  *   q [T][n_q_heads][head_dim] bf16, token rows q_stride apart; n_q_heads = 0
  *     (q, q_out NULL): keys and values only
  *   k, v [T][n_kv_heads][head_dim] bf16, token rows k_stride, v_stride apart
@@ -484,10 +490,12 @@ size_t attn_workspace_bytes(const kv_cache* cache, int32_t n_seqs, int32_t q_len
  * -inf; one with a NaN score (in q, or in K at a key it sees) gives NaN.  What the
  * cache holds at keys that a row does not see (NaN included) does not enter it.  A
  * page number outside the cache hides its keys and sets MOE_STATUS_BAD_PAGE.
- * Scores and sums are fp32.  For the product with V a key's weight is rounded to
- * bf16; in an E4M3 cache the weight times the key's V scale to fp16, by 2^-11 of
+ * Scores and sums are fp32.  K and V of an E2M1 cache become bf16 exactly.  For the
+ * product with V a key's weight is rounded to bf16; in an E4M3 cache the weight times the key's V scale to fp16, by 2^-11 of
  * itself or by 2^-29 of the row's largest if that is more (V scales up to 2^80
  * apart).
+ * Sums are formed of weights up to 8 and divided at the end: |v| times 8 times the
+ * keys has to stay within fp32's range.
  * n_seqs * q_len <= 262144, n_q_heads <= 1024, n_seqs * q_len * n_q_heads < 2^24
  * and max_keys <= 2^28. */
 int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t n_seqs,

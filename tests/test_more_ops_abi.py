@@ -136,3 +136,21 @@ def test_logits_null_rules_and_binding_errors():
         moe.lora_linear(w, P, 64, 1, P, None, 0, P, 64, 1, None, P, BIG, stream=0)
     with pytest.raises(moe.MoeError):
         moe.logits_adjust(moe.make_logits_rules(), P, 1, 9, 1, 10, P, 1, 10, None, stream=0)
+
+
+def test_a_cache_in_4_bits_has_its_scales():
+    def rc(**o):
+        a = dict(dt=4, n=10, page=16, Hkv=2, D=64, k=P, v=P, ks=P, vs=P)
+        a.update(o)
+        c = ctypes.byref(moe.make_kv_cache(a["dt"], a["n"], a["page"], a["Hkv"], a["D"], a["k"], a["v"],
+                                           a["ks"], a["vs"]))
+        app = moe.raw_call("kv_append_rope", c, P, 256, 4, P, 128, P, 128, 0, None, 0, 0, 0, P, P, P, 2, 4,
+                           P, None, None)
+        att = moe.raw_call("attn_shared_prefix", c, P, 256, 0, 1, 4, P, P, 20, P, 4, 64, 0.1, P, None,
+                           None, None, 0, None)
+        assert app == att
+        assert (moe._lib.attn_workspace_bytes(c, 2, 1, 4, 20, 64) > 0) == (app == OK)
+        return app
+    assert rc() == OK
+    assert rc(ks=None) == EINVAL and rc(vs=None) == EINVAL and rc(dt=5) == EINVAL
+    assert rc(ks=P + 8) == EALIGN and rc(D=96) == ENOTSUP and rc(page=8) == ENOTSUP
