@@ -176,11 +176,14 @@ struct LoraArgs {
   const void* base;        // or null
   void* y;
   float* h;                // [parts][T][R] partial sums of a x
+  uint16_t* op;            // many tokens: [T][3][R] their sum times the scale, in three parts
   uint32_t* status;
   int64_t x_stride, base_stride, y_stride;
-  int T, K, N, R, n, parts, steps;  // steps: of 32 columns a wave takes at a time (1, 2, 4, 8)
-  int part_cols;           // columns of x in a part
+  int T, K, N, R, n;
+  int parts, part_cols;    // parts of the columns of x
+  int h_slots, h_groups;   // set by the launcher
   bool y_bf16, in_place;
+  bool many;               // tokens enough that a tile's adapters are taken in turn
 };
 hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
 

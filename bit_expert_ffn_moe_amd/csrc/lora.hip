@@ -45,81 +45,94 @@ constexpr int kWaves = 8;  // of the first kernel
 
 }  // namespace
 
-// h: grid (parts, tiles of 16 tokens, slots).  A wave takes 32 S columns at a time, of
-// which x stays in registers for all the tile's adapters and their ranks; adapters of the
-// tile are dealt out over the slots.
-template <int S>
+// h: grid (parts, tiles of 16 TT tokens, slots x groups of 32 ranks).  A wave takes 32 S
+// columns at a time, of which x stays in registers for all the adapters that the block
+// takes: those of its tile are dealt out over the slots, their ranks over the groups (many
+// tokens: one slot, one group).
+template <int S, int TT>
 __global__ __launch_bounds__(64 * kWaves) void lora_h_kernel(LoraArgs a) {
-  __shared__ float red[kWaves][4][4][64];
+  constexpr int NT = 16 * TT;
+  __shared__ float red[kWaves][2][TT][4][64];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int t0 = blockIdx.y * 16;
+  const int t0 = blockIdx.y * NT;
+  const int slots = a.h_slots, first_slot = blockIdx.z % slots, group = blockIdx.z / slots;
   bool bad = false;
-  const int id = adapter_at(a, t0, c, bad);
-  if (a.status && bad && blockIdx.x == 0 && blockIdx.z == 0 && wv == 0)
-    set_status(a.status, MOE_STATUS_BAD_INDEX);
+  const int id = adapter_at(a, t0, lane & (NT - 1), bad);
   const int k_lo = blockIdx.x * a.part_cols, k_hi = min(a.K, k_lo + a.part_cols);
   const int passes = (k_hi - k_lo + 256 * S - 1) / (256 * S);
-  const uint16_t* xr = a.x + (size_t)min(t0 + c, a.T - 1) * a.x_stride;
-  uint4 x[S];
-  // (columns past the end: 0 on both sides)
+  uint4 x[TT][S];
+  // (columns past the end: 0 on both sides; with slots, of the block's tokens alone)
   auto column = [&](int p, int s) { return k_lo + ((p * kWaves + wv) * S + s) * 32 + 8 * g; };
-  auto load_x = [&](int p) {
+  auto load_x = [&](int p, uint32_t of) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int k = column(p, s);
-      x[s] = *reinterpret_cast<const uint4*>(xr + min(k, a.K - 8));
-      if (k >= k_hi) x[s] = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < TT; ++j) {
+      const uint16_t* xr = a.x + (size_t)min(t0 + 16 * j + c, a.T - 1) * a.x_stride;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const int k = column(p, s);
+        x[j][s] = make_uint4(0, 0, 0, 0);
+        if (k < k_hi && (of >> (16 * j + c) & 1u)) x[j][s] = *reinterpret_cast<const uint4*>(xr + k);
+      }
     }
   };
-  if (passes == 1) load_x(0);
+  if (passes == 1 && slots == 1) load_x(0, 0xffffffffu);
+  if (a.status && bad && blockIdx.x == 0 && blockIdx.z == 0 && wv == 0)
+    set_status(a.status, MOE_STATUS_BAD_INDEX);
 
-  uint32_t left = (uint32_t)__ballot(id >= 0) & 0xffffu;
+  const uint32_t all = NT == 32 ? 0xffffffffu : 0xffffu;
+  uint32_t left = (uint32_t)__ballot(id >= 0) & all;
   for (int slot = 0; left; ++slot) {
     const int i = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    const uint32_t mine = (uint32_t)__ballot(id == i) & 0xffffu;
+    const uint32_t mine = (uint32_t)__ballot(id == i) & all;
     left &= ~mine;
-    if (slot % (int)gridDim.z != (int)blockIdx.z) continue;
+    if (slot % slots != first_slot) continue;
     const int rank = rank_of(a, i);
     const uint16_t* wa = a.a + (size_t)i * a.R * a.K;
-    for (int r0 = 0; r0 < a.R; r0 += 64) {  // four tiles of 16 ranks
-      v4f_t acc[4];
+    for (int r0 = 32 * group; r0 < a.R; r0 += 32 * a.h_groups) {  // two tiles of 16 ranks
+      v4f_t acc[2][TT];
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) acc[rt] = v4f_t{0.f, 0.f, 0.f, 0.f};
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
       for (int p = 0; p < passes; ++p) {
-        if (passes > 1) load_x(p);
+        if (passes > 1 || (slots > 1 && r0 == 32 * group)) load_x(p, slots > 1 ? mine : 0xffffffffu);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-          if (r0 + 16 * rt < rank) {
-            const uint16_t* row = wa + (size_t)min(r0 + 16 * rt + c, rank - 1) * a.K;
+        for (int rt = 0; rt < 2; ++rt)
+          // (the first ranks do not wait for the rank's number)
+          if (r0 + 16 * rt < (r0 + rt ? rank : a.R)) {
+            const uint16_t* row = wa + (size_t)min(r0 + 16 * rt + c, a.R - 1) * a.K;
             uint4 w[S];
 #pragma unroll
             for (int s = 0; s < S; ++s) {
               const int k = column(p, s);
-              w[s] = *reinterpret_cast<const uint4*>(row + min(k, a.K - 8));
-              if (k >= k_hi) w[s] = make_uint4(0, 0, 0, 0);
+              w[s] = make_uint4(0, 0, 0, 0);
+              if (k < k_hi) w[s] = *reinterpret_cast<const uint4*>(row + k);
             }
 #pragma unroll
-            for (int s = 0; s < S; ++s) acc[rt] = mfma(w[s], x[s], acc[rt]);
+            for (int j = 0; j < TT; ++j)
+#pragma unroll
+              for (int s = 0; s < S; ++s) acc[rt][j] = mfma(w[s], x[j][s], acc[rt][j]);
           }
       }
       // the waves' sums, four consecutive ranks of a token a thread
       __syncthreads();
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-        if (r0 + 16 * rt < rank)
+      for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) red[wv][rt][e][lane] = acc[rt][e];
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) red[wv][rt][j][e][lane] = acc[rt][j][e];
       __syncthreads();
-      const int tok = threadIdx.x >> 4, rt = (threadIdx.x >> 2) & 3, q = threadIdx.x & 3;
+      const int q = threadIdx.x & 3, rt = (threadIdx.x >> 2) & 1, tok = threadIdx.x >> 3;
       const int r = r0 + 16 * rt + 4 * q;
-      if (threadIdx.x < 256 && (mine >> tok & 1u) && r < a.R) {
+      if (tok < NT && (mine >> tok & 1u) && r < a.R) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (r + e < rank)
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) v[e] += red[w][rt][e][16 * q + tok];
+            for (int w = 0; w < kWaves; ++w) v[e] += red[w][rt][tok >> 4][e][16 * q + (tok & 15)];
         *reinterpret_cast<float4*>(a.h + ((size_t)blockIdx.x * a.T + t0 + tok) * a.R + r) =
             make_float4(v[0], v[1], v[2], v[3]);
       }
@@ -138,163 +151,314 @@ __device__ __forceinline__ void cut3(float v, uint32_t (&p)[3]) {
   p[2] = __float_as_uint(d - __uint_as_float(p[1])) & 0xffff0000u;
 }
 
+// Four consecutive outputs at element `at`, which has their alignment only, as words: two of
+// bf16 pairs or four of fp32.
 template <bool BF16>
-__device__ __forceinline__ void load16(const void* p, size_t at, float (&v)[16]) {
+struct Four {
+  uint32_t w[BF16 ? 2 : 4];
+};
+template <bool BF16>
+__device__ __forceinline__ Four<BF16> load4(const void* p, size_t at) {
+  Four<BF16> f;
+  memcpy(f.w, (const uint8_t*)p + at * (BF16 ? 2 : 4), sizeof f.w);
+  return f;
+}
+// y = base + d at four outputs
+template <bool BF16>
+__device__ __forceinline__ void store4(void* p, size_t at, const Four<BF16>& base, float d0, float d1,
+                                       float d2, float d3) {
+  Four<BF16> o;
   if constexpr (BF16) {
-    uint32_t w[8];
-    memcpy(w, (const uint16_t*)p + at, sizeof w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = bf16_to_f32(w[i] & 0xffffu);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    o.w[0] = f32x2_to_bf16x2(bf16_to_f32(base.w[0] & 0xffffu) + d0,
+                             __uint_as_float(base.w[0] & 0xffff0000u) + d1);
+    o.w[1] = f32x2_to_bf16x2(bf16_to_f32(base.w[1] & 0xffffu) + d2,
+                             __uint_as_float(base.w[1] & 0xffff0000u) + d3);
   } else {
-    memcpy(v, (const float*)p + at, sizeof v);
+    o.w[0] = __float_as_uint(__uint_as_float(base.w[0]) + d0);
+    o.w[1] = __float_as_uint(__uint_as_float(base.w[1]) + d1);
+    o.w[2] = __float_as_uint(__uint_as_float(base.w[2]) + d2);
+    o.w[3] = __float_as_uint(__uint_as_float(base.w[3]) + d3);
+  }
+  memcpy((uint8_t*)p + at * (BF16 ? 2 : 4), o.w, sizeof o.w);
+}
+// the same where fewer than four are left
+template <bool BF16>
+__device__ __forceinline__ void store_some(const LoraArgs& a, int t, int n, const float (&d)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (n + k >= a.N) break;
+    const size_t at = (size_t)t * a.y_stride + n + k, ab = (size_t)t * a.base_stride + n + k;
+    float v = d[k];
+    if (a.base) v += BF16 ? bf16_to_f32(((const uint16_t*)a.base)[ab]) : ((const float*)a.base)[ab];
+    if (BF16)
+      ((uint16_t*)a.y)[at] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+    else
+      ((float*)a.y)[at] = v;
   }
 }
 
+// The first operand of the second product: h of token t (a row per lane, l%16) at the ranks
+// of lane group g, parts added up in order, times the adapter's scale, cut in three along
+// the k axis.  MODE: how many times 8 ranks the k axis holds before it starts over with the
+// next part: 1, 2 or 4 (NB blocks of 32 ranks).
+template <int MODE, int NB>
+struct Rows {
+  static constexpr int NP = MODE == 1 ? 1 : MODE == 2 ? 2 : 3;  // products per block of ranks
+  uint4 op[NB][NP];
+  __device__ __forceinline__ void load(const LoraArgs& a, int t, int g, bool mine, float sc) {
+    const int ro = 8 * (g & (MODE - 1));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int r = 32 * b + ro;
+      float h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = 0.0f;
+      if (mine && r < a.R)
+        for (int p0 = 0; p0 < a.parts; p0 += 4) {
+          float4 u[4], v[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float* hp = a.h + ((size_t)min(p0 + p, a.parts - 1) * a.T + t) * a.R + r;
+            u[p] = *reinterpret_cast<const float4*>(hp), v[p] = *reinterpret_cast<const float4*>(hp + 4);
+          }
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if (p0 + p < a.parts) {
+              h[0] += u[p].x, h[1] += u[p].y, h[2] += u[p].z, h[3] += u[p].w;
+              h[4] += v[p].x, h[5] += v[p].y, h[6] += v[p].z, h[7] += v[p].w;
+            }
+        }
+      uint32_t p[3][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t q[3];
+        cut3(h[e] * sc, q);
+        p[0][e] = q[0], p[1][e] = q[1], p[2][e] = q[2];
+      }
+      auto pack = [&](int k) {
+        return make_uint4(p[k][0] >> 16 | p[k][1], p[k][2] >> 16 | p[k][3],
+                          p[k][4] >> 16 | p[k][5], p[k][6] >> 16 | p[k][7]);
+      };
+      const uint4 zero = make_uint4(0, 0, 0, 0), p0 = pack(0), p1 = pack(1), p2 = pack(2);
+      if constexpr (MODE == 1) {
+        op[b][0] = g == 0 ? p0 : g == 1 ? p1 : g == 2 ? p2 : zero;
+      } else if constexpr (MODE == 2) {
+        op[b][0] = g < 2 ? p0 : p1;
+        op[b][1] = g < 2 ? p2 : zero;
+      } else {
+        op[b][0] = p0, op[b][1] = p1, op[b][2] = p2;
+      }
+    }
+  }
+  // The same from a.op, where lora_op_kernel left the three parts of a token one behind the
+  // other: along the k axis as well.
+  __device__ __forceinline__ void load_ready(const LoraArgs& a, int t, int g) {
+    const uint4* p = reinterpret_cast<const uint4*>(a.op) + (size_t)t * 3 * (a.R >> 3);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int pieces = a.R >> 3;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if constexpr (MODE == 1) {
+        op[b][0] = g < 3 ? p[g] : zero;
+      } else if constexpr (MODE == 2) {
+        op[b][0] = p[g];
+        op[b][1] = g < 2 ? p[4 + g] : zero;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          op[b][q] = p[q * pieces + min(4 * b + g, pieces - 1)];
+          if (4 * b + g >= pieces) op[b][q] = zero;
+        }
+      }
+    }
+  }
+  // d[k] += products with w(b, k), the weights of output k; those past the rank may be anything
+  template <class W>
+  __device__ __forceinline__ void multiply(int g, int rank, W&& w, v4f_t (&d)[4]) const {
+    const int ro = 8 * (g & (MODE - 1));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (32 * b >= rank) break;
+      const int r = 32 * b + ro;
+      uint32_t keep[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        keep[e] = (r + 2 * e < rank ? 0xffffu : 0u) | (r + 2 * e + 1 < rank ? 0xffff0000u : 0u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 x = w(b, k);
+        x.x &= keep[0], x.y &= keep[1], x.z &= keep[2], x.w &= keep[3];
+#pragma unroll
+        for (int p = NP - 1; p >= 0; --p) d[k] = mfma(op[b][p], x, d[k]);
+      }
+    }
+  }
+};
+
 }  // namespace
 
-// y: grid (64 outputs a wave, tiles of 16 tokens, slots).  MODE: how many times 8 ranks the
-// k axis holds before it starts over with the next part of h: 1, 2 or 4 (NB blocks of 32
-// ranks).  Row m of product i is output n0 + 16 (m / 4) + 4 i + m % 4, so that a lane ends
-// with 16 consecutive outputs of its token.
+// The operands of many tokens, formed once: four ranks of a token a thread.
+__global__ __launch_bounds__(256) void lora_op_kernel(LoraArgs a) {
+  const int per = a.R >> 2;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(at / per), r = 4 * (int)(at % per);
+  if (t >= a.T) return;
+  const int id = a.of[t];
+  if (id < 0 || id >= a.n) return;  // (its row of the products is not looked at)
+  float h[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < a.parts; ++p) {
+    const float4 u = *reinterpret_cast<const float4*>(a.h + ((size_t)p * a.T + t) * a.R + r);
+    h[0] += u.x, h[1] += u.y, h[2] += u.z, h[3] += u.w;
+  }
+  const float sc = a.scale ? a.scale[id] : 1.0f;
+  uint32_t q[4][3];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) cut3(h[e] * sc, q[e]);
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+    *reinterpret_cast<uint2*>(a.op + ((size_t)t * 3 + p) * a.R + r) =
+        make_uint2(q[0][p] >> 16 | q[1][p], q[2][p] >> 16 | q[3][p]);
+}
+
+// y, few tokens: grid (64 outputs a wave, tiles of 16 tokens, slots).  Tokens are the rows of
+// the result, output n0 + 4 (l%16) + k the column of product k: a lane ends with four
+// consecutive outputs of tokens 4 (l/16) .. + 3, 16 lanes with 64 consecutive ones.
 template <int MODE, int NB, bool BF16>
 __global__ __launch_bounds__(256) void lora_y_kernel(LoraArgs a) {
-  constexpr int NP = MODE == 1 ? 1 : MODE == 2 ? 2 : 3;  // products per block of ranks
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int t0 = blockIdx.y * 16, n0 = (blockIdx.x * 4 + wv) * 64;
+  const int t0 = blockIdx.y * 16, n0 = (blockIdx.x * 4 + wv) * 64, n = n0 + 4 * c;
   if (n0 >= a.N) return;
   bool bad;
   const int id = adapter_at(a, t0, c, bad);
-  const int t = min(t0 + c, a.T - 1);
-  // this lane's outputs n.. n + 15
-  const int n = n0 + 16 * g;
-  const bool whole = n + 16 <= a.N;
-  float v0[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) v0[j] = 0.0f;
-  if (a.base) {
-    const size_t at = (size_t)t * a.base_stride + n;
-    if (whole) {
-      load16<BF16>(a.base, at, v0);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (n + j < a.N)
-          v0[j] = BF16 ? bf16_to_f32(((const uint16_t*)a.base)[at + j])
-                       : ((const float*)a.base)[at + j];
-    }
-  }
-  // h of this lane's token at its ranks, parts added up in order
-  const int ro = 8 * (g & (MODE - 1));
-  float h[NB][8];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[b][e] = 0.0f;
-  if (id >= 0)
-    for (int p = 0; p < a.parts; ++p) {
-      const float* hp = a.h + ((size_t)p * a.T + t) * a.R;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int r = 32 * b + ro;
-        if (r < a.R) {
-          const float4 u = *reinterpret_cast<const float4*>(hp + r);
-          const float4 v = *reinterpret_cast<const float4*>(hp + r + 4);
-          h[b][0] += u.x, h[b][1] += u.y, h[b][2] += u.z, h[b][3] += u.w;
-          h[b][4] += v.x, h[b][5] += v.y, h[b][6] += v.z, h[b][7] += v.w;
-        }
-      }
-    }
-  const float sc = id >= 0 && a.scale ? a.scale[id] : 1.0f;
-  uint4 op[NB][NP];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    uint32_t p[3][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t q[3];
-      cut3(h[b][e] * sc, q);
-      p[0][e] = q[0], p[1][e] = q[1], p[2][e] = q[2];
-    }
-    auto pack = [&](int k) {
-      return make_uint4(p[k][0] >> 16 | p[k][1], p[k][2] >> 16 | p[k][3], p[k][4] >> 16 | p[k][5],
-                        p[k][6] >> 16 | p[k][7]);
-    };
-    const uint4 zero = make_uint4(0, 0, 0, 0), p0 = pack(0), p1 = pack(1), p2 = pack(2);
-    if constexpr (MODE == 1) {
-      op[b][0] = g == 0 ? p0 : g == 1 ? p1 : g == 2 ? p2 : zero;
-    } else if constexpr (MODE == 2) {
-      op[b][0] = g < 2 ? p0 : p1;
-      op[b][1] = g < 2 ? p2 : zero;
-    } else {
-      op[b][0] = p0, op[b][1] = p1, op[b][2] = p2;
-    }
-  }
-
-  auto finish = [&](const v4f_t (&d)[4]) {
-    float v[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = v0[j] + d[j >> 2][j & 3];
-    const size_t at = (size_t)t * a.y_stride + n;
-    if (whole) {
-      if constexpr (BF16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = f32x2_to_bf16x2(v[2 * j], v[2 * j + 1]);
-        memcpy((uint16_t*)a.y + at, w, sizeof w);
-      } else {
-        memcpy((float*)a.y + at, v, sizeof v);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (n + j < a.N) {
-          if (BF16)
-            ((uint16_t*)a.y)[at + j] = (uint16_t)f32x2_to_bf16x2(v[j], 0.0f);
-          else
-            ((float*)a.y)[at + j] = v[j];
-        }
-    }
-  };
-
   uint32_t left = (uint32_t)__ballot(id >= (a.in_place ? 0 : -1)) & 0xffffu;
   for (int slot = 0; left; ++slot) {
     const int i = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    left &= ~(uint32_t)__ballot(id == i);
+    const uint32_t ours = (uint32_t)__ballot(id == i) & 0xffffu;
+    left &= ~ours;
     if (slot % (int)gridDim.z != (int)blockIdx.z) continue;
+    Four<BF16> base[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      memset(&base[e], 0, sizeof base[e]);
+      if (a.base && (ours >> (4 * g + e) & 1u) && n + 4 <= a.N)
+        base[e] = load4<BF16>(a.base, (size_t)(t0 + 4 * g + e) * a.base_stride + n);
+    }
     v4f_t d[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) d[k] = v4f_t{0.f, 0.f, 0.f, 0.f};
     if (i >= 0) {
-      const int rank = rank_of(a, i);
       const uint16_t* wb = a.b + (size_t)i * a.N * a.R;
+      const int ro = 8 * (g & (MODE - 1));
+      uint4 w[NB][4];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (32 * b >= rank) break;
-        const int r = 32 * b + ro;
-        uint4 w[4];
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = min(n0 + 16 * (c >> 2) + 4 * k + (c & 3), a.N - 1);
-          w[k] = *reinterpret_cast<const uint4*>(wb + (size_t)row * a.R + min(r, a.R - 8));
-        }
-        // weights past the rank may be anything
-        uint32_t keep[4];
+        for (int k = 0; k < 4; ++k)
+          w[b][k] = *reinterpret_cast<const uint4*>(wb + (size_t)min(n + k, a.N - 1) * a.R +
+                                                    min(32 * b + ro, a.R - 8));
+      const int rank = rank_of(a, i);
+      Rows<MODE, NB> rows;
+      rows.load(a, min(t0 + c, a.T - 1), g, id == i, a.scale ? a.scale[i] : 1.0f);
+      rows.multiply(g, rank, [&](int b, int k) { return w[b][k]; }, d);
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          keep[e] = (r + 2 * e < rank ? 0xffffu : 0u) | (r + 2 * e + 1 < rank ? 0xffff0000u : 0u);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          w[k].x &= keep[0], w[k].y &= keep[1], w[k].z &= keep[2], w[k].w &= keep[3];
-#pragma unroll
-          for (int p = NP - 1; p >= 0; --p) d[k] = mfma(w[k], op[b][p], d[k]);
-        }
+    for (int e = 0; e < 4; ++e) {
+      if (!(ours >> (4 * g + e) & 1u)) continue;
+      const int t = t0 + 4 * g + e;
+      if (n + 4 <= a.N) {
+        store4<BF16>(a.y, (size_t)t * a.y_stride + n, base[e], d[0][e], d[1][e], d[2][e], d[3][e]);
+      } else {
+        const float v[4] = {d[0][e], d[1][e], d[2][e], d[3][e]};
+        store_some<BF16>(a, t, n, v);
       }
     }
-    if (id == i) finish(d);
+  }
+}
+
+// y, many tokens: grid (64 NC outputs, 64 tokens).  A wave takes 16 of the tokens; the
+// adapter's weights of these outputs, which lie together in memory, come through LDS for all
+// of them, their 16-byte pieces permuted by row so that the 16 lanes of a group, four
+// rows apart, meet distinct banks.  What does not wait for the adapter's number (base, h) is
+// loaded first, the next adapter's weights under this one's products.
+template <int MODE, int NB, bool BF16, int NC>
+__global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
+  constexpr int PR = 4 * NB;                  // pieces of a row in LDS (R / 8 of them are there)
+  constexpr int NL = NB * NC;                 // pieces a thread loads
+  __shared__ uint4 lw[64 * NC * PR];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int tb = blockIdx.y * 64, t0 = tb + 16 * wv, n0 = blockIdx.x * 64 * NC;
+  bool bad;
+  const int id = adapter_at(a, tb, lane, bad);  // of the block's token l
+  // four outputs of four tokens a chunk; those past the last token stand in as the last
+  Four<BF16> base[NC][4];
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      memset(&base[j][e], 0, sizeof base[j][e]);
+      if (a.base && n0 + 64 * j + 64 <= a.N)
+        base[j][e] = load4<BF16>(a.base, (size_t)min(t0 + 4 * g + e, a.T - 1) * a.base_stride + n0 + 64 * j + 4 * c);
+    }
+  Rows<MODE, NB> rows;
+  rows.load_ready(a, min(t0 + c, a.T - 1), g);
+
+  auto place = [](int row, int piece) { return (row * PR + piece) ^ ((row >> 2) & 15); };
+  const int pieces = a.R >> 3;                // of a row in memory
+  const int ro = g & (MODE - 1);
+  uint4 wreg[NL];
+  auto load_w = [&](int i) {
+    const uint4* wb = reinterpret_cast<const uint4*>(a.b) + (size_t)i * a.N * pieces;
+    const size_t from = (size_t)n0 * pieces, last = (size_t)a.N * pieces - 1;
+#pragma unroll
+    for (int l = 0; l < NL; ++l) {
+      const size_t at = from + min(l * 256 + (int)threadIdx.x, 64 * NC * pieces - 1);
+      wreg[l] = wb[at < last ? at : last];
+    }
+  };
+  uint64_t left = __ballot(id >= (a.in_place ? 0 : -1));
+  int i = left ? __builtin_amdgcn_readlane(id, __builtin_ctzll(left)) : -1;
+  if (i >= 0) load_w(i);
+  while (left) {
+    const uint64_t all = __ballot(id == i);
+    const uint32_t ours = (uint32_t)(all >> (16 * wv)) & 0xffffu;
+    left &= ~all;
+    const int next = left ? __builtin_amdgcn_readlane(id, __builtin_ctzll(left)) : -1;
+    if (i >= 0) {
+      __syncthreads();  // (the adapter before is done with LDS)
+#pragma unroll
+      for (int l = 0; l < NL; ++l) {
+        const int j = l * 256 + threadIdx.x;
+        if (j < 64 * NC * pieces) lw[place(j / pieces, j % pieces)] = wreg[l];
+      }
+      __syncthreads();
+    }
+    if (next >= 0) load_w(next);
+    const int rank = i >= 0 ? rank_of(a, i) : 0;
+    if (ours)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int n = n0 + 64 * j + 4 * c;
+        v4f_t d[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[k] = v4f_t{0.f, 0.f, 0.f, 0.f};
+        rows.multiply(g, rank, [&](int b, int k) {
+          return lw[place(64 * j + 4 * c + k, min(4 * b + ro, pieces - 1))];
+        }, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!(ours >> (4 * g + e) & 1u)) continue;
+          const int t = t0 + 4 * g + e;
+          if (n0 + 64 * j + 64 <= a.N) {
+            store4<BF16>(a.y, (size_t)t * a.y_stride + n, base[j][e], d[0][e], d[1][e], d[2][e], d[3][e]);
+          } else {
+            const float v[4] = {d[0][e], d[1][e], d[2][e], d[3][e]};
+            store_some<BF16>(a, t, n, v);
+          }
+        }
+      }
+    i = next;
   }
 }
 
@@ -303,38 +467,48 @@ namespace {
 int clamp_to(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : (int)v; }
 
 template <int MODE, int NB>
-void launch_y(const LoraArgs& a, dim3 grid, hipStream_t st) {
-  if (a.y_bf16)
-    lora_y_kernel<MODE, NB, true><<<grid, 256, 0, st>>>(a);
-  else
-    lora_y_kernel<MODE, NB, false><<<grid, 256, 0, st>>>(a);
+void launch_y(const LoraArgs& a, int slots, hipStream_t st) {
+  if (a.many) {
+    constexpr int NC = 1;
+    const dim3 grid((a.N + 64 * NC - 1) / (64 * NC), (a.T + 63) / 64);
+    if (a.y_bf16)
+      lora_y_many_kernel<MODE, NB, true, NC><<<grid, 256, 0, st>>>(a);
+    else
+      lora_y_many_kernel<MODE, NB, false, NC><<<grid, 256, 0, st>>>(a);
+  } else {
+    const dim3 grid((a.N + 255) / 256, (a.T + 15) / 16, slots);
+    if (a.y_bf16)
+      lora_y_kernel<MODE, NB, true><<<grid, 256, 0, st>>>(a);
+    else
+      lora_y_kernel<MODE, NB, false><<<grid, 256, 0, st>>>(a);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_lora(const LoraArgs& a, hipStream_t st) {
-  const int tiles = (a.T + 15) / 16, most = min(min(a.T, 16), a.n);
-  const dim3 gh(a.parts, tiles, clamp_to(1024 / ((int64_t)a.parts * tiles), 1, most));
-  if (a.steps == 1)
-    lora_h_kernel<1><<<gh, 64 * kWaves, 0, st>>>(a);
-  else if (a.steps == 2)
-    lora_h_kernel<2><<<gh, 64 * kWaves, 0, st>>>(a);
-  else if (a.steps == 4)
-    lora_h_kernel<4><<<gh, 64 * kWaves, 0, st>>>(a);
-  else
-    lora_h_kernel<8><<<gh, 64 * kWaves, 0, st>>>(a);
-  const int nb = (a.N + 255) / 256;
-  const dim3 gy(nb, tiles, clamp_to(2048 / ((int64_t)nb * tiles), 1, min(most + 1, 16)));
+hipError_t launch_lora(const LoraArgs& args, hipStream_t st) {
+  LoraArgs a = args;
+  const int most = a.T < 16 ? a.T : 16, different = most < a.n ? most : a.n;
+  if (a.many) {
+    a.h_slots = a.h_groups = 1;
+    lora_h_kernel<4, 2><<<dim3(a.parts, (a.T + 31) / 32), 64 * kWaves, 0, st>>>(a);
+    lora_op_kernel<<<(unsigned)(((int64_t)a.T * (a.R / 4) + 255) / 256), 256, 0, st>>>(a);
+  } else {
+    const int tiles = (a.T + 15) / 16;
+    a.h_slots = different, a.h_groups = (a.R + 31) / 32;
+    lora_h_kernel<4, 1><<<dim3(a.parts, tiles, a.h_slots * a.h_groups), 64 * kWaves, 0, st>>>(a);
+  }
+  const int slots = clamp_to(different + (a.in_place ? 0 : 1), 1, most);
   if (a.R <= 8)
-    launch_y<1, 1>(a, gy, st);
+    launch_y<1, 1>(a, slots, st);
   else if (a.R <= 16)
-    launch_y<2, 1>(a, gy, st);
+    launch_y<2, 1>(a, slots, st);
   else if (a.R <= 32)
-    launch_y<4, 1>(a, gy, st);
+    launch_y<4, 1>(a, slots, st);
   else if (a.R <= 64)
-    launch_y<4, 2>(a, gy, st);
+    launch_y<4, 2>(a, slots, st);
   else
-    launch_y<4, 4>(a, gy, st);
+    launch_y<4, 4>(a, slots, st);
   return hipGetLastError();
 }
 

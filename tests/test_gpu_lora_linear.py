@@ -90,12 +90,27 @@ def test_ranks(R, out):
 @pytest.mark.parametrize("T,K,N,n,R", [(1, 4096, 300, 2, 16), (32, 2056, 500, 32, 64), (300, 600, 128, 6, 32),
                                        (1500, 264, 70, 3, 8), (4100, 72, 40, 9, 16), (3, 70000, 17, 3, 8)])
 def test_sizes(T, K, N, n, R):
-    """The splits of x's columns: 1 to 8 steps a wave, several parts, several passes a part (70000)."""
+    """Few tokens and many (from 1024), several parts of x's columns, several passes a part."""
     rng = np.random.default_rng(T)
     x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, "bf16", True, pad=8)
     check(x, a, b, rank, scale, of, base, "bf16", ys=N + 3)
     of = torch.from_numpy((np.arange(T) * n // T).astype(np.int32))      # runs of one adapter
     check(x, a, b, rank, scale, of, base, "bf16", in_place=True)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [8, 16, 32, 64, 104, 128])
+def test_many_tokens(R, out):
+    """Every rank's kernels for many tokens (from 1024): chunks of outputs cut short, a last block of few
+    tokens, one or many adapters a block."""
+    rng = np.random.default_rng(R)
+    for T, K, N, n in [(1024, 1104, 700, 2), (1415, 72, 64, 30), (1090, 4104, 257, 5), (1025, 2048, 33, 1),
+                       (2000, 136, 3, 70)]:
+        print(R, out, T, K, N, n, flush=True)
+        x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, out, True)
+        check(x, a, b, rank, scale, of, base, out)
+        of = torch.from_numpy((np.arange(T) * n // T).astype(np.int32))
+        check(x, a, b, None, scale, of, base, out, in_place=True)
 
 
 @pytest.mark.parametrize("R", [8, 16, 64])
