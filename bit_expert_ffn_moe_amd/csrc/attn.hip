@@ -304,20 +304,34 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
   // two groups share one); a lane's V columns of 8 keys as loaded, and the scale bytes of
   // all columns of these keys
   constexpr int KW = D / 32, VSW = D / 32;
-  uint32_t kq[2][KW], ksb[2], vq[8][D == 256 ? 2 : 1], vsb[2][VSW];
-  auto load_k = [&](const Rows& r) {
-    if constexpr (FP4) {
+  struct Raw {
+    uint32_t kq[2][KW], ksb[2], vq[8][D == 256 ? 2 : 1], vsb[2][VSW];
+  };
+  auto load_k4 = [&](const Rows& r, Raw& raw) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        load_dwords((const uint8_t*)a.k + r.row[u] * RB + ko, kq[u]);
-        const uint8_t* sb = (const uint8_t*)a.ks + r.row[u] * SB;
-        if constexpr (D == 256)
-          ksb[u] = *reinterpret_cast<const uint16_t*>(sb + c * SB + 2 * g);
-        else
-          ksb[u] = sb[c * SB + (D == 64 ? g >> 1 : g)];
-      }
-      return;
+    for (int u = 0; u < 2; ++u) {
+      load_dwords((const uint8_t*)a.k + r.row[u] * RB + ko, raw.kq[u]);
+      const uint8_t* sb = (const uint8_t*)a.ks + r.row[u] * SB;
+      if constexpr (D == 256)
+        raw.ksb[u] = *reinterpret_cast<const uint16_t*>(sb + c * SB + 2 * g);
+      else
+        raw.ksb[u] = sb[c * SB + (D == 64 ? g >> 1 : g)];
     }
+  };
+  auto load_v4 = [&](const Rows& r, Raw& raw) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint8_t* vb = (const uint8_t*)a.v + r.row[e >> 2] * RB + vo + (e & 3) * RB;
+      if constexpr (D == 64)
+        raw.vq[e][0] = *reinterpret_cast<const uint16_t*>(vb);
+      else
+        load_dwords(vb, raw.vq[e]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      load_dwords((const uint8_t*)a.vs + (r.row[u] + 4 * g) * SB, raw.vsb[u]);
+  };
+  auto load_k = [&](const Rows& r) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint8_t* kb = (const uint8_t*)a.k + r.row[u] * RB;
@@ -330,41 +344,27 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     }
   };
   auto load_v = [&](const Rows& r) {
-    if constexpr (FP4) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint8_t* vb = (const uint8_t*)a.v + r.row[e >> 2] * RB + vo + (e & 3) * RB;
-        if constexpr (D == 64)
-          vq[e][0] = *reinterpret_cast<const uint16_t*>(vb);
-        else
-          load_dwords(vb, vq[e]);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        load_dwords((const uint8_t*)a.vs + (r.row[u] + 4 * g) * SB, vsb[u]);
-      return;
-    }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       load_dwords((const uint8_t*)a.v + r.row[e >> 2] * RB + vo + (e & 3) * RB, vr[e]);
   };
   // E2M1 V as bf16, from here on as if loaded so
-  auto widen_v = [&] {
+  auto widen_v = [&](const Raw& raw) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       // byte VD c / 32 of the row's scale bytes, which are half a dword, one or two
-      const uint32_t w = D == 64    ? vsb[e >> 2][(e & 3) >> 1] >> 16 * (e & 1)
-                         : D == 128 ? vsb[e >> 2][e & 3]
-                         : c < 8    ? vsb[e >> 2][(2 * (e & 3)) % VSW]
-                                    : vsb[e >> 2][(2 * (e & 3) + 1) % VSW];
+      const uint32_t w = D == 64    ? raw.vsb[e >> 2][(e & 3) >> 1] >> 16 * (e & 1)
+                         : D == 128 ? raw.vsb[e >> 2][e & 3]
+                         : c < 8    ? raw.vsb[e >> 2][(2 * (e & 3)) % VSW]
+                                    : raw.vsb[e >> 2][(2 * (e & 3) + 1) % VSW];
       const float sc = fp4_scale(w >> 8 * (VD * c / 32 & 3) & 0xffu);
       if constexpr (D == 64) {
-        const uint4 x = fp4x8(vq[e][0], sc);
+        const uint4 x = fp4x8(raw.vq[e][0], sc);
         vr[e][0] = x.x, vr[e][1 % VW] = x.y;
       } else {
 #pragma unroll
         for (int i = 0; i < VW; i += 4) {
-          const uint4 x = fp4x8(vq[e][i / 4], sc);
+          const uint4 x = fp4x8(raw.vq[e][i / 4], sc);
           vr[e][i] = x.x, vr[e][(i + 1) % VW] = x.y, vr[e][(i + 2) % VW] = x.z,
           vr[e][(i + 3) % VW] = x.w;
         }
@@ -400,8 +400,9 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
 
   // One tile, its K and V loaded (or on their way): SLOW, one limit at a time.
   // `after_k` and `after_v` run when K and V are dead.  False: nothing was done,
-  // the tile needs SLOW.
-  auto tile = [&](auto slow, int j0, const Rows& cur, auto&& after_k, auto&& after_v) -> bool {
+  // the tile needs SLOW (E2M1: and the next tile's loads are the caller's).
+  auto tile = [&](auto slow, int j0, const Rows& cur, const Raw& raw, auto&& after_k,
+                  auto&& after_v) -> bool {
     constexpr bool SLOW = decltype(slow)::value;
     const bool bad = cur.bad[0] || cur.bad[1];
     if (bad && lane == 0 && a.status) set_status(a.status, MOE_STATUS_BAD_PAGE);
@@ -410,10 +411,15 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     auto key_of = [&](int e) { return j0 + 16 * (e >> 2) + 4 * g + (e & 3); };
     auto inside = [&](int e) { return key_of(e) >= lo && key_of(e) < hi && !cur.bad[e >> 2]; };
 
-    if constexpr (FP4 && !SLOW) widen_v();  // (SLOW: widened and cleared before)
+    // (E2M1: the wait for V is here only where it has to be looked at; SLOW: widened and
+    // cleared before)
+    if constexpr (FP4 && !SLOW)
+      if (edge) widen_v(raw);
     if (!SLOW && edge && leaks(j0, cur)) {
-      after_k();
-      after_v();
+      if constexpr (!FP4) {
+        after_k();
+        after_v();
+      }
       return false;
     }
 
@@ -426,7 +432,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           if constexpr (FP4) {
-            kf[u][s] = fp4x8(kq[u][s], fp4_scale(D == 256 ? ksb[u] >> 8 * (s >> 2) & 0xffu : ksb[u]));
+            kf[u][s] = fp4x8(raw.kq[u][s], fp4_scale(D == 256 ? raw.ksb[u] >> 8 * (s >> 2) & 0xffu : raw.ksb[u]));
           } else if constexpr (FP8) {
             const uint4 k = kr[u][s / 2];
             kf[u][s] = (s & 1) ? fp8x8(k.z, k.w) : fp8x8(k.x, k.y);
@@ -525,6 +531,10 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
       p[rt] = pack_p<FP8>(w);
     }
 
+    if constexpr (FP4 && !SLOW) {
+      if (!edge) widen_v(raw);
+      after_v();
+    }
     // O^T += V^T P^T, column set j of the lanes
     auto v_operand = [&](int j) -> uint4 {
       uint32_t d[4];
@@ -577,13 +587,36 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
         }
       }
     }
-    after_v();
+    if (!FP4) after_v();
     return true;
   };
 
   const int step = 128, first = (lo & ~31) + 32 * wv;
   bool leaked = false;
-  {
+  Raw ring;
+  if constexpr (FP4) {
+    // (no branch guards a load, so that a wait leaves the younger in flight; past the last
+    // key any row serves)
+    if (first < hi) {
+      Rows cur = rows_at(first);
+      load_k4(cur, ring);
+      __builtin_amdgcn_sched_barrier(0);  // (in the order of the loop, or its waits count wrong)
+      load_v4(cur, ring);
+#pragma unroll 1
+      for (int j0 = first; j0 < hi; j0 += step) {
+        const Rows nxt = rows_at(j0 + step);
+        if (!tile(std::false_type{}, j0, cur, ring, [&] { load_k4(nxt, ring); },
+                  [&] { load_v4(nxt, ring); })) {
+          // (in the tile these loads would be waited for by the code behind it)
+          leaked = true;
+          load_k4(nxt, ring);
+          __builtin_amdgcn_sched_barrier(0);
+          load_v4(nxt, ring);
+        }
+        cur = nxt;
+      }
+    }
+  } else {
     Rows cur{}, nxt{};
     if (first < hi) {
       cur = rows_at(first);
@@ -593,7 +626,7 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     for (int j0 = first; j0 < hi; j0 += step) {
       const bool more = j0 + step < hi;
       if (more) nxt = rows_at(j0 + step);
-      leaked |= !tile(std::false_type{}, j0, cur, [&] { if (more) load_k(nxt); },
+      leaked |= !tile(std::false_type{}, j0, cur, ring, [&] { if (more) load_k(nxt); },
                       [&] { if (more) load_v(nxt); });
       cur = nxt;
     }
@@ -603,10 +636,15 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
     for (int j0 = first; j0 < hi; j0 += step) {
       const Rows cur = rows_at(j0);
       if (!(j0 < lo || j0 + 32 > min(hi, minlim) || cur.bad[0] || cur.bad[1])) continue;
-      load_k(cur);
-      load_v(cur);
-      if constexpr (FP4) widen_v();
-      if (leaks(j0, cur)) tile(std::true_type{}, j0, cur, [] {}, [] {});
+      if constexpr (FP4) {
+        load_k4(cur, ring);
+        load_v4(cur, ring);
+        widen_v(ring);
+      } else {
+        load_k(cur);
+        load_v(cur);
+      }
+      if (leaks(j0, cur)) tile(std::true_type{}, j0, cur, ring, [] {}, [] {});
     }
   }
 
