@@ -58,9 +58,21 @@ namespace {
 // blocks of 32), of 32 rows up to 128 (128 rows: 23.7 us, 29.0 in blocks of 16, whose
 // repeated reads of K and V L2 then bounds), keys through LDS above (512 rows over
 // 32768 keys: 114 us, 189 in blocks of 32).
-void split_rows(int rows, int D, int* kind, int* blocks) {
-  if (rows <= 128) {
+//
+// E2M1 keys cost more vector work than bytes.  Key tiles, which widen them once for all rows
+// but keep two waves a SIMD waiting for each other, pay later: 256 rows over 8192 keys at 128
+// columns 29.5 us in blocks of 32, 47.6 through LDS; 512 rows 51.3 and 67.3; 512 rows over
+// 32768 keys 140 and 125.  Blocks of 16 rows (three waves a SIMD, 32 rows leave two) carry 65
+// to 128 rows where the prefix is short (2000 keys: 15.0 us, 16.0) or, at 128 columns, the
+// sequences' own keys in the same launch are the most (8192 shared, 32 x 2048 own: 25.6, 30.4;
+// 16384 shared, 8 x 1024 own: 34.1, 28.8).
+void split_rows(const kv_cache* c, int rows, int keys, int64_t others, int* kind, int* blocks) {
+  const int D = c->head_dim;
+  const bool e2m1 = c->dtype == MOE_DT_FP4_E2M1 && D < 256;
+  const int few = !e2m1 ? 128 : keys <= 16384 ? 512 : 256;
+  if (rows <= few) {
     *kind = rows <= 64 || D == 256 ? 1 : 2;
+    if (e2m1 && rows <= 128 && (keys < 8192 || (D == 128 && others > (int64_t)4 * keys))) *kind = 1;
     *blocks = ceil_div(rows, 16 * *kind);
   } else {
     *kind = kAttnTile;
@@ -102,8 +114,10 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   a->n_pages = c->n_pages, a->page_shift = log2_of(c->page_size);
   a->prefix_len = prefix_len, a->max_keys = max_keys;
   a->kv = kv_kind(c);
-  split_rows(a->n_tok * a->G, a->D, &a->prefix_kind, &a->prefix_blocks);
-  split_rows(q_len * a->G, a->D, &a->own_kind, &a->own_blocks);
+  const int own_keys = max_keys - prefix_len;
+  split_rows(c, a->n_tok * a->G, prefix_len, (int64_t)n_seqs * own_keys, &a->prefix_kind,
+             &a->prefix_blocks);
+  split_rows(c, q_len * a->G, own_keys, 0, &a->own_kind, &a->own_blocks);
   const int base_p = a->Hkv * a->prefix_blocks;
   // blocks wanted: a prefix one per CU, all together four per CU (half of each at
   // 256 columns, whose blocks take twice the registers)

@@ -13,6 +13,15 @@ pytestmark = pytest.mark.gpu
 
 import bit_expert_ffn_moe_amd as moe  # noqa: E402
 
+# beside the other types' shapes: rows enough (over 512 of a kv head) for key tiles in LDS at 64 and 128
+# columns, for the shared keys, a sequence's own and both
+TILES = [
+    (5, 40, 16, 2, 128, 16, 300, [40, 64, 150, 90, 77]),
+    (2, 600, 2, 2, 64, 32, 100, [600, 700]),
+    (1, 520, 1, 1, 128, 64, 0, [777]),
+    (66, 4, 8, 4, 64, 128, 130, [4 + i % 7 for i in range(66)]),
+]
+
 DEV = "cuda:0"
 FP4 = moe.MOE_DT_FP4_E2M1
 MAG = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])
@@ -188,7 +197,7 @@ def test_append_padding_and_out_of_range():
 
 # ---- attention --------------------------------------------------------------------
 
-@pytest.mark.parametrize("shape", FEW + SHAPES)
+@pytest.mark.parametrize("shape", FEW + SHAPES + TILES)
 def test_matches_64_bit_attention(shape):
     B, Q, Hq, Hkv, D, page, P, own = shape
     print(shape, flush=True)
@@ -204,7 +213,7 @@ def test_scales_of_all_sizes(D):
     """Scale bytes over their whole range in V, block by block (the values' own tolerance holds for
     each output column by itself), and over a range that scores bear in K."""
     rng = np.random.default_rng(D)
-    for B, Q, G in ((3, 1, 4), (3, 50, 4)):            # few rows, many rows
+    for B, Q, G in ((3, 1, 4), (3, 50, 4), (3, 180, 4)):   # few rows, more, many
         P, own = 150, [30 + Q, 64 + Q, 1 + Q]
         kv, q, pre, table, n = build4(rng, B, Q, G, 1, D, 32, P, own)
         shape = kv.t["vs"].shape
@@ -218,9 +227,9 @@ def test_scales_of_all_sizes(D):
         eo, el, mag, qk = ref.attention(q.double().numpy(), kv, pos, pre, P, table, 0.05, Q, n)
         d = 2 * D * 2.0 ** -23 * qk
         tol = 1.05 * 2.0 ** -8 * (mag + np.abs(eo)) + (2 * d[..., None] + 2.0 ** -16) * mag + 2.0 ** -134
-        # sums are formed of weights up to 8 before they are divided: 8 x 264 keys x 6 x 2^(byte - 127)
-        # is below fp32's 2^128 up to byte 241; beyond that a sum may be infinite where out is not
-        fits = np.repeat(kv.t["vs"][0, 0, 0].numpy() <= 241, 32)
+        # sums are formed of weights up to 8 before they are divided: 8 x 394 keys x 6 x 2^(byte - 127)
+        # is below fp32's 2^128 up to byte 240; beyond that a sum may be infinite where out is not
+        fits = np.repeat(kv.t["vs"][0, 0, 0].numpy() <= 240, 32)
         assert fits.sum() >= D - 32
         assert (np.abs(o - eo) <= tol)[..., fits].all()
         assert (np.abs(lse - el) <= d + 2.0 ** -20 * (1 + np.abs(el))).all()
@@ -230,7 +239,7 @@ def test_scales_of_all_sizes(D):
 def test_one_key_gives_its_value_at_every_scale(D):
     """A row of one key has weight 1: out is V, whatever its scale byte (0 to 252)."""
     rng = np.random.default_rng(D)
-    for B, P in ((1, 0), (140, 1)):                    # few rows, many rows
+    for B, P in ((1, 0), (140, 1), (520, 1)):          # few rows, more, many
         kv, q, pre, table, n = build4(rng, B, 1, 1, 1, D, 16, P, [1 - P] * B)
         pg = int(pre[0]) if P else int(table[0, 0])
         for lo in range(0, 253, D // 32):
@@ -249,7 +258,7 @@ def test_limits_inside_the_prefix_and_empty_rows():
     check(o, lse, q, kv, pos, pre, P, table, 0.125, Q, n)
     o, lse = call(kv, q, np.full(12, -1), pre, P, table, n, 0.125, Q)
     assert (o == 0).all() and (lse == -np.inf).all()
-    for shape in MANY:
+    for shape in MANY + TILES:
         B, Q, Hq, Hkv, D, page, P, own = shape
         kv, q, pre, table, n = build4(rng, B, Q, Hq, Hkv, D, page, P, own)
         pos = np.minimum(rng.integers(-30, n, B * Q), np.repeat([P + m for m in own], Q) - 1)
@@ -258,7 +267,7 @@ def test_limits_inside_the_prefix_and_empty_rows():
 
 
 @pytest.mark.parametrize("byte", [253, 254, 255])
-@pytest.mark.parametrize("shape", MANY + [FEW[5], FEW[6], FEW[8]])
+@pytest.mark.parametrize("shape", MANY + TILES[:3] + [FEW[5], FEW[6], FEW[8]])
 def test_what_a_row_does_not_see_does_not_enter(shape, byte):
     """NaN blocks in the free part of pages, and in one block of V at the keys of the sequences' last
     rows: those rows alone turn NaN, in that block's columns alone."""
@@ -302,7 +311,7 @@ def test_a_nan_key_that_a_row_sees_gives_nan():
 
 def test_bad_pages():
     rng = np.random.default_rng(9)
-    for shape in MANY[:2] + [FEW[4]]:
+    for shape in MANY[:2] + TILES[:2] + [FEW[4]]:
         B, Q, Hq, Hkv, D, page, P, own = shape
         kv, q, pre, table, n = build4(rng, B, Q, Hq, Hkv, D, page, P, own)
         pos = positions(own, P, Q)
