@@ -95,25 +95,31 @@ __global__ __launch_bounds__(64 * kWaves) void lora_h_kernel(LoraArgs a) {
       for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
         for (int j = 0; j < TT; ++j) acc[rt][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
-      for (int p = 0; p < passes; ++p) {
+      for (int p = 0; p < (r0 && r0 >= rank ? 0 : passes); ++p) {
         if (passes > 1 || (slots > 1 && r0 == 32 * group)) load_x(p, slots > 1 ? mine : 0xffffffffu);
+        // Both tiles' weights on their way together (the first ranks' do not wait for the rank's
+        // number)
+        uint4 w[2][S];
+        const bool two = r0 + 16 < rank;
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt)
-          // (the first ranks do not wait for the rank's number)
-          if (r0 + 16 * rt < (r0 + rt ? rank : a.R)) {
-            const uint16_t* row = wa + (size_t)min(r0 + 16 * rt + c, a.R - 1) * a.K;
-            uint4 w[S];
+        for (int rt = 0; rt < 2; ++rt) {
+          if (rt && !two) break;
+          const uint16_t* row = wa + (size_t)min(r0 + 16 * rt + c, a.R - 1) * a.K;
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-              const int k = column(p, s);
-              w[s] = make_uint4(0, 0, 0, 0);
-              if (k < k_hi) w[s] = *reinterpret_cast<const uint4*>(row + k);
-            }
-#pragma unroll
-            for (int j = 0; j < TT; ++j)
-#pragma unroll
-              for (int s = 0; s < S; ++s) acc[rt][j] = mfma(w[s], x[j][s], acc[rt][j]);
+          for (int s = 0; s < S; ++s) {
+            const int k = column(p, s);
+            w[rt][s] = make_uint4(0, 0, 0, 0);
+            if (k < k_hi) w[rt][s] = *reinterpret_cast<const uint4*>(row + k);
           }
+        }
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+          if (rt && !two) break;
+#pragma unroll
+          for (int j = 0; j < TT; ++j)
+#pragma unroll
+            for (int s = 0; s < S; ++s) acc[rt][j] = mfma(w[rt][s], x[j][s], acc[rt][j]);
+        }
       }
       // the waves' sums, four consecutive ranks of a token a thread
       __syncthreads();
