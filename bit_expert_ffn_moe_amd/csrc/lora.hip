@@ -52,7 +52,7 @@ constexpr int kWaves = 8;  // of the first kernel
 template <int S, int TT>
 __global__ __launch_bounds__(64 * kWaves) void lora_h_kernel(LoraArgs a) {
   constexpr int NT = 16 * TT;
-  __shared__ float red[kWaves][2][TT][4][64];
+  __shared__ v4f_t red[kWaves][2][TT][64];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.y * NT;
@@ -126,21 +126,17 @@ __global__ __launch_bounds__(64 * kWaves) void lora_h_kernel(LoraArgs a) {
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int j = 0; j < TT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) red[wv][rt][j][e][lane] = acc[rt][j][e];
+        for (int j = 0; j < TT; ++j) red[wv][rt][j][lane] = acc[rt][j];
       __syncthreads();
-      const int q = threadIdx.x & 3, rt = (threadIdx.x >> 2) & 1, tok = threadIdx.x >> 3;
-      const int r = r0 + 16 * rt + 4 * q;
-      if (tok < NT && (mine >> tok & 1u) && r < a.R) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+      const int rt = wv & 1, j = wv >> 1, tok = 16 * j + c, r = r0 + 16 * rt + 4 * g;
+      if (j < TT && (mine >> tok & 1u) && r < a.R) {
+        v4f_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) v += red[w][rt][j][lane];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (r + e < rank)
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) v[e] += red[w][rt][tok >> 4][e][16 * q + (tok & 15)];
-        *reinterpret_cast<float4*>(a.h + ((size_t)blockIdx.x * a.T + t0 + tok) * a.R + r) =
-            make_float4(v[0], v[1], v[2], v[3]);
+          if (r + e >= rank) v[e] = 0.0f;
+        *reinterpret_cast<v4f_t*>(a.h + ((size_t)blockIdx.x * a.T + t0 + tok) * a.R + r) = v;
       }
     }
   }
