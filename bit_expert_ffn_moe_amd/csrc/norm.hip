@@ -10,6 +10,11 @@
 // A sum of squares past fp32's range (|r| from 2^57 on at 16384 columns) is formed again
 // in units of the row's largest power of two; small squares need no such care, since eps
 // >= 2^-100 is far above what underflow loses.
+//
+// Bound by HBM where tokens are many: 8192 of 4096 columns with residual, E4M3 and scales, 302
+// MB read and written in 56.3 us, 5.4 TB/s, what a copy of that size takes.  A few tokens
+// cost a launch, one trip to memory and one through LDS (2.8 us at 4096 columns, which is less
+// than the caller's thread takes to launch it).
 #include "common.h"
 #include "kernels.h"
 #include "vec8.h"
@@ -150,18 +155,25 @@ void launch_nv(const NormArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// A row's time is the latency of its loads and of the block's sum, so a thread has one chunk
+// of 8 where a block can have that many threads (1024 columns, 64 rows: 2.7 us so, 3.3 with
+// two; 2048: 2.7 and 3.5; 4096: 3.1 and 3.6; 8192: 4.6 and 4.7, 5.5 with four).  Thousands
+// of rows of up to 4096 columns stream faster from smaller blocks (4096 rows of 4096: 28.0 us
+// with two chunks a thread, 29.3 with one; 2048 rows 16.4 and 15.9).
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
   const int nch = a.H >> 3;
   if (nch <= 64)
     launch_nv<64, 1>(a, st);
   else if (nch <= 128)
-    launch_nv<64, 2>(a, st);
+    launch_nv<128, 1>(a, st);
   else if (nch <= 256)
     launch_nv<256, 1>(a, st);
-  else if (nch <= 512)
+  else if (nch <= 512 && a.T > 2048)
     launch_nv<256, 2>(a, st);
+  else if (nch <= 512)
+    launch_nv<512, 1>(a, st);
   else if (nch <= 1024)
-    launch_nv<512, 2>(a, st);
+    launch_nv<1024, 1>(a, st);
   else
     launch_nv<1024, 2>(a, st);
   return hipGetLastError();

@@ -193,3 +193,13 @@ def test_other_stream_and_captured():
         g.replay()
         torch.cuda.synchronize()
         check(x, r, w, 1e-6, H, T, [t.cpu() for t in (ro, y, q, s)])
+
+
+@pytest.mark.parametrize("res", ["bf16", "f32", None])
+def test_thousands_of_rows_of_up_to_4096_columns(res):
+    """The blocks of 256 threads with two chunks each."""
+    rng = np.random.default_rng(6)
+    for T, H in ((2049, 2176), (2100, 4096)):
+        print(T, H, res, flush=True)
+        x, r, w = make(rng, T, H, res)
+        check(x, r, w, 1e-6, H, T, call(x, r, w, 1e-6, H, T, True, True))

@@ -266,3 +266,13 @@ def test_captured_beside_eager_calls():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(o.view(torch.int32), e.view(torch.int32))
+
+
+@pytest.mark.parametrize("zdt,odt", [("bf16", "f32"), ("f32", "bf16")])
+def test_blocks_of_8192_ids_into_the_other_type(zdt, odt):
+    rng = np.random.default_rng(11)
+    T, V = 70, 16411
+    z = logits(rng, T, V, zdt)
+    r = rules_of(rng, T, V, 900, 20, True, seqs=3)
+    for shift in (0, 1):
+        check(r, z, V, odt, pad_out=3, shift=shift)
