@@ -32,6 +32,19 @@
 // TB/s in all: the shared keys are read by four blocks of rows, from L2 but for the
 // first).  16 sequences of 4 tokens, 8 kv heads of 8 query heads each, 32768 shared
 // E4M3 keys and up to 1024 of their own, 70 GFLOP: 133 us.
+//
+// E2M1 keys and values are widened to bf16 on the way to the matrix cores, by the codes' own
+// scale (v_cvt_scalef32_pk_bf16_fp4, four for 8 codes), which is exact: what follows is bf16
+// attention over what the cache holds.  A lane's 8 V codes come as a dword, and their permutes
+// are those of bf16.  Two tiles of 16 bytes less a lane hide less latency, so the next tile's
+// codes are loaded before this tile's products: without a branch and in the order in which they
+// are wanted, so that a wait for one leaves the later ones on their way.  Bound by vector
+// instructions (widening, softmax) and those waits, not by bytes: 8 sequences of 8 kv heads
+// and 8 query heads each over up to 65536 keys of 128 columns, 241 MB, in 59 us (4.1 TB/s;
+// issue 54% busy) and 5 for the join; 32 sequences, 4 query heads each, behind 8192 shared
+// keys, up to 2048 of their own, 43 MB, in 21.5 us and 4.  In the first more or fewer parts took 69 to 114 us, a third tile in flight 70 to 102 (the
+// loop's code then no longer fits the instruction cache beside the rest), one wave more a SIMD
+// 164 (registers spilled).
 #include <type_traits>
 
 #include "common.h"
