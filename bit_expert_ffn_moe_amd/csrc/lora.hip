@@ -50,7 +50,8 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int i) {
   return a.rank ? max(0, min(a.rank[i], a.R)) : a.R;
 }
 
-constexpr int kWaves = 8;  // of the first kernel
+constexpr int kWaves = 8;       // of the first kernel
+constexpr int kOneCols = 4096;  // columns of x that lora_one_kernel takes
 
 }  // namespace
 
@@ -473,6 +474,87 @@ __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
   }
 }
 
+// A few tokens of small adapters, in one launch: grid (512 outputs, tokens).  Every block forms
+// its token's h again, columns over the waves, all of A on its way at once (x in the
+// products' first column, the others' results are not looked at); rows of B and base
+// arrive meanwhile, and an output is a thread's dot product with h.  P: pieces of 8 ranks.
+template <int P, bool BF16>
+__global__ __launch_bounds__(64 * kWaves) void lora_one_kernel(LoraArgs a) {
+  constexpr int S = kOneCols / (32 * kWaves), RT = (P + 1) / 2;
+  __shared__ v4f_t red[kWaves][RT][4];
+  __shared__ float hs[16 * RT];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int t = blockIdx.y, n = blockIdx.x * 64 * kWaves + threadIdx.x;
+  const int i = a.of[t];
+  if (i >= a.n && a.status && blockIdx.x == 0 && threadIdx.x == 0)
+    set_status(a.status, MOE_STATUS_BAD_INDEX);
+  const bool has = i >= 0 && i < a.n;
+  if (!has && a.in_place) return;
+  const size_t at = (size_t)t * a.y_stride + n;
+  float y = 0.0f;
+  if (a.base && n < a.N) {
+    const size_t ab = (size_t)t * a.base_stride + n;
+    y = BF16 ? bf16_to_f32(((const uint16_t*)a.base)[ab]) : ((const float*)a.base)[ab];
+  }
+  if (has) {
+    const uint4* wb = reinterpret_cast<const uint4*>(a.b) + ((size_t)i * a.N + min(n, a.N - 1)) * (a.R >> 3);
+    uint4 b[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) b[p] = wb[min(p, (a.R >> 3) - 1)];
+    const int rank = rank_of(a, i);
+    const uint16_t* xr = a.x + (size_t)t * a.x_stride;
+    const uint16_t* wa = a.a + (size_t)i * a.R * a.K;
+    v4f_t acc[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) acc[rt] = v4f_t{0.f, 0.f, 0.f, 0.f};
+    uint4 x[S], w[RT][S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int k = ((s >> 1) * kWaves + wv) * 64 + (s & 1) * 32 + 8 * g;
+      x[s] = make_uint4(0, 0, 0, 0);
+      if (k < a.K && c == 0) x[s] = *reinterpret_cast<const uint4*>(xr + k);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        w[rt][s] = make_uint4(0, 0, 0, 0);
+        if (k < a.K && 16 * rt + c < a.R)
+          w[rt][s] = *reinterpret_cast<const uint4*>(wa + (size_t)(16 * rt + c) * a.K + k);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) acc[rt] = mfma(w[rt][s], x[s], acc[rt]);
+    if (c == 0)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) red[wv][rt][g] = acc[rt];
+    __syncthreads();
+    if (threadIdx.x < 16 * RT) {
+      float h = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) h += reinterpret_cast<const float*>(red[w])[threadIdx.x];
+      hs[threadIdx.x] = h * (a.scale ? a.scale[i] : 1.0f);
+    }
+    __syncthreads();
+    float d = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t u[4] = {b[p].x, b[p].y, b[p].z, b[p].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * p + e < rank)
+          d = fmaf(hs[8 * p + e], e & 1 ? __uint_as_float(u[e / 2] & 0xffff0000u)
+                                        : bf16_to_f32(u[e / 2] & 0xffffu), d);
+    }
+    y += d;
+  }
+  if (n >= a.N) return;
+  if (BF16)
+    ((uint16_t*)a.y)[at] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
+  else
+    ((float*)a.y)[at] = y;
+}
+
 namespace {
 
 int clamp_to(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : (int)v; }
@@ -495,10 +577,33 @@ void launch_y(const LoraArgs& a, int slots, hipStream_t st) {
   }
 }
 
+template <int P>
+void launch_one(const LoraArgs& a, hipStream_t st) {
+  const dim3 grid((a.N + 64 * kWaves - 1) / (64 * kWaves), a.T);
+  if (a.y_bf16)
+    lora_one_kernel<P, true><<<grid, 64 * kWaves, 0, st>>>(a);
+  else
+    lora_one_kernel<P, false><<<grid, 64 * kWaves, 0, st>>>(a);
+}
+
 }  // namespace
 
 hipError_t launch_lora(const LoraArgs& args, hipStream_t st) {
   LoraArgs a = args;
+  // One launch where a block's A comes faster than a second launch and there is a CU for every block
+  // (a CU alone pulls some 45 bytes a ns).  4096 x 4096, 1 token: rank 8 5.6 us so, 6.7 in two launches; rank 16
+  // 7.0 and 7.1 (the calling thread saves a launch); rank 32 10.9 and 8.1.  1024 x 1024, rank 32, 32
+  // tokens: 5.5 and 9.1.  4096 x 14336, rank 8: 8 tokens 5.8 and 7.8, 16 tokens (448 blocks) 10.9 and 8.5.
+  const int64_t blocks = (int64_t)a.T * ((a.N + 64 * kWaves - 1) / (64 * kWaves));
+  if (a.K <= kOneCols && (int64_t)a.R * a.K <= 1 << 16 && a.R <= 32 && blocks <= 256) {
+    if (a.R <= 8)
+      launch_one<1>(a, st);
+    else if (a.R <= 16)
+      launch_one<2>(a, st);
+    else
+      launch_one<4>(a, st);
+    return hipGetLastError();
+  }
   const int most = a.T < 16 ? a.T : 16, different = most < a.n ? most : a.n;
   if (a.many) {
     a.h_slots = a.h_groups = 1;

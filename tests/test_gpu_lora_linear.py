@@ -231,3 +231,39 @@ def test_captured_beside_eager_calls_with_a_workspace_each():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [8, 16, 24, 32])
+def test_one_launch_or_two(R, out):
+    """Small adapters at both sides of the limits of tokens times outputs, columns and both: one kernel
+    for up to 256 blocks of 512 outputs and 65536 elements of a, two beyond."""
+    rng = np.random.default_rng(R)
+    for T, K, N, n in [(256, 72, 40, 7), (257, 72, 40, 7), (300, 1000, 65, 40), (1, 2048, 1500, 3), (2, 2056, 515, 2),
+                       (1, 4096, 33, 2), (3, 4104, 100, 2), (19, 6000, 130, 30), (40, 264, 5000, 9)]:
+        print(R, out, T, K, N, n, flush=True)
+        x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, out, True, pad=8)
+        check(x, a, b, rank, scale, of, base, out, ys=N + 1)
+        check(x, a, b, None, None, of, base, out, in_place=True)
+
+
+def test_two_launches_and_what_is_not_the_tokens():
+    """The same of NaN, infinities and bad numbers in two launches: tokens enough."""
+    rng = np.random.default_rng(12)
+    T, K, N, n, R = 270, 136, 90, 5, 32
+    x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, "f32", pad=8)
+    rank = torch.tensor([32, 7, 0, 17, 25], dtype=torch.int32)
+    of = torch.from_numpy(np.tile(np.array([0, 1, 2, 3, -1], np.int32), 54))
+    want = check(x, a, b, rank, scale, of, base, "f32")
+    for i in range(n):
+        r = int(rank[i])
+        a[i, r:], b[i, :, r:] = float("nan"), float("inf")
+    a[4], b[4], x[:, K:], scale[4] = float("nan"), float("nan"), float("nan"), float("nan")
+    x[0], x[6, 3], x[4] = float("nan"), float("inf"), float("nan")
+    of[8], of[263] = n, 2 ** 31 - 1
+    y, st = run(x, a, b, rank, scale, of, base, "f32")
+    assert st == moe.MOE_STATUS_BAD_INDEX
+    same = torch.ones(T, dtype=torch.bool)
+    same[0] = same[6] = same[8] = same[263] = False
+    assert torch.equal(y[same], want[same]) and torch.equal(y[[8, 263]], base[[8, 263], :N])
+    assert bool(y[0].isnan().all()) and not bool(y[6].isfinite().any())
