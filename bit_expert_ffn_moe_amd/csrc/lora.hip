@@ -1,8 +1,9 @@
 // lora.hip -- low-rank adapters of many requests beside a projection that they share:
 //   y[t] = base[t] + s_i B_i (A_i x[t]),  i = adapter_of[t].
 //
-// Two kernels: h = A_i x in parts of the columns of x (fp32, in the workspace), then y =
-// base + s_i B_i h, where the parts are added up.  Both take tiles of 16 tokens with
+// Two kernels (one for a few tokens of small adapters: lora_one_kernel): h = A_i x in parts of
+// the columns of x (fp32, in the workspace), then y = base + s_i B_i h, where the parts are
+// added up.  Both take tiles of 16 tokens with
 // v_mfma_f32_16x16x32_bf16, the adapter's weights as the first operand (lane: row l%16, 8
 // consecutive k from 8 (l/16)) and the tokens as the columns of the second, so a token's
 // results are a column of its own.  A tile's different adapters are multiplied in turn
@@ -14,18 +15,19 @@
 // parts that add up to it exactly (8 bits each, cut off), along the k axis where the
 // rank leaves room: a rank of 8 takes one instruction, 16 two, 32 three.
 //
-// 4096 tokens of 6 adapters in runs, 4096 x 4096, rank 32, 104 MB and 2.1 GFLOP (HBM alone: 20 us): 38.8
-// us, of which h takes 14.2 (x read once, 35 MB; every block reads its adapters' A from L2, as many
-// bytes as x), its operands 4.7 and y 20.0 (70 MB; every block of 64 x 64 outputs reads its part of B
-// and its tokens' operands from L2; the vector unit is busy 57% with that and base + d).  Outputs of 128
-// or 256 columns a block halve or quarter the operands' reads but leave fewer waves a SIMD: 46 and
-// 57 us.  32 tokens of 24 adapters, ranks up to 64, 4096 x 6144, are a read of their weights (18.7 MB:
-// 3.3 us): h 6.0, y 8.6, each a launch and three dependent trips to memory (numbers, rank and weights, result).  One
-// token: 3.7 and 4.3 us, two launches.
+// 4096 tokens of 6 adapters in runs, 4096 x 4096, rank 32, 104 MB and 2.1 GFLOP (HBM alone: 20
+// us): 38.8 us, of which h takes 14.2 (x read once, 35 MB; every block reads its adapters' A
+// from L2, as many bytes as x), its operands 4.7 and y 20.0 (70 MB; every block of 64 x 64
+// outputs reads its part of B and its tokens' operands from L2; the vector unit is busy 57%
+// with that and base + d).  Outputs of 128 or 256 columns a block halve or quarter the
+// operands' reads but leave fewer waves a SIMD: 46 and 57 us.  32 tokens of 24 adapters, ranks
+// up to 64, 4096 x 6144, are a read of their weights (18.7 MB: 3.3 us): h 6.0, y 8.6, each a
+// launch and three dependent trips to memory (numbers, rank and weights, result).
 #include <string.h>
 
 #include "common.h"
 #include "kernels.h"
+#include "vec8.h"
 
 namespace bef {
 
@@ -50,8 +52,7 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int i) {
   return a.rank ? max(0, min(a.rank[i], a.R)) : a.R;
 }
 
-constexpr int kWaves = 8;       // of the first kernel
-constexpr int kOneCols = 4096;  // columns of x that lora_one_kernel takes
+constexpr int kWaves = 8;  // of the first kernel
 
 }  // namespace
 
@@ -475,14 +476,14 @@ __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
 }
 
 // A few tokens of small adapters, in one launch: grid (512 outputs, tokens).  Every block forms
-// its token's h again, columns over the waves, all of A on its way at once (x in the
-// products' first column, the others' results are not looked at); rows of B and base
-// arrive meanwhile, and an output is a thread's dot product with h.  P: pieces of 8 ranks.
+// its token's h again on the vector unit, 4096 columns of all ranks on their way at once, a wave
+// 1 KB of a row of A at a time (as a matrix operand, 16 rows of 64 bytes at a time, A of
+// 131 KB took 2.5 us more); rows of B and base arrive meanwhile, and an output is a
+// thread's dot product with h.  P: pieces of 8 ranks.
 template <int P, bool BF16>
 __global__ __launch_bounds__(64 * kWaves) void lora_one_kernel(LoraArgs a) {
-  constexpr int S = kOneCols / (32 * kWaves), RT = (P + 1) / 2;
-  __shared__ v4f_t red[kWaves][RT][4];
-  __shared__ float hs[16 * RT];
+  __shared__ float red[kWaves][8 * P];
+  __shared__ float hs[8 * P];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int t = blockIdx.y, n = blockIdx.x * 64 * kWaves + threadIdx.x;
@@ -505,35 +506,52 @@ __global__ __launch_bounds__(64 * kWaves) void lora_one_kernel(LoraArgs a) {
     const int rank = rank_of(a, i);
     const uint16_t* xr = a.x + (size_t)t * a.x_stride;
     const uint16_t* wa = a.a + (size_t)i * a.R * a.K;
-    v4f_t acc[RT];
+    float h[8 * P];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) acc[rt] = v4f_t{0.f, 0.f, 0.f, 0.f};
-    uint4 x[S], w[RT][S];
+    for (int r = 0; r < 8 * P; ++r) h[r] = 0.0f;
+    for (int k = 8 * threadIdx.x; k < a.K; k += 512 * kWaves) {
+      const uint4 xw = *reinterpret_cast<const uint4*>(xr + k);
+      uint4 w[8 * P];
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int k = ((s >> 1) * kWaves + wv) * 64 + (s & 1) * 32 + 8 * g;
-      x[s] = make_uint4(0, 0, 0, 0);
-      if (k < a.K && c == 0) x[s] = *reinterpret_cast<const uint4*>(xr + k);
+      for (int r = 0; r < 8 * P; ++r)
+        w[r] = *reinterpret_cast<const uint4*>(wa + (size_t)min(r, a.R - 1) * a.K + k);
+      float xf[8];
+      unpack8(xw, xf);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        w[rt][s] = make_uint4(0, 0, 0, 0);
-        if (k < a.K && 16 * rt + c < a.R)
-          w[rt][s] = *reinterpret_cast<const uint4*>(wa + (size_t)(16 * rt + c) * a.K + k);
+      for (int r = 0; r < 8 * P; ++r) {
+        float wf[8];
+        unpack8(w[r], wf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[r] = fmaf(wf[e], xf[e], h[r]);
       }
     }
+    // halves, then quarters of the wave exchange two ranks' sums and keep one each
 #pragma unroll
-    for (int s = 0; s < S; ++s)
+    for (int r = 0; r < 4 * P; ++r) {
+      const auto z = __builtin_amdgcn_permlane32_swap(__float_as_uint(h[r]),
+                                                      __float_as_uint(h[r + 4 * P]), false, false);
+      h[r] = __uint_as_float(z[0]) + __uint_as_float(z[1]);
+    }
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) acc[rt] = mfma(w[rt][s], x[s], acc[rt]);
-    if (c == 0)
+    for (int r = 0; r < 2 * P; ++r) {
+      const auto z = __builtin_amdgcn_permlane16_swap(__float_as_uint(h[r]),
+                                                      __float_as_uint(h[r + 2 * P]), false, false);
+      h[r] = __uint_as_float(z[0]) + __uint_as_float(z[1]);
+    }
+    // lane group g has ranks r + 2 P (g & 1) + 4 P (g >> 1)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) red[wv][rt][g] = acc[rt];
+    for (int r = 0; r < 2 * P; ++r) {
+      float v = h[r];
+#pragma unroll
+      for (int o = 1; o < 16; o *= 2) v += __shfl_xor(v, o, 16);
+      if (c == 0) red[wv][r + 2 * P * (g & 1) + 4 * P * (g >> 1)] = v;
+    }
     __syncthreads();
-    if (threadIdx.x < 16 * RT) {
-      float h = 0.0f;
+    if (threadIdx.x < 8 * P) {
+      float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) h += reinterpret_cast<const float*>(red[w])[threadIdx.x];
-      hs[threadIdx.x] = h * (a.scale ? a.scale[i] : 1.0f);
+      for (int u = 0; u < kWaves; ++u) v += red[u][threadIdx.x];
+      hs[threadIdx.x] = v * (a.scale ? a.scale[i] : 1.0f);
     }
     __syncthreads();
     float d = 0.0f;
@@ -590,12 +608,13 @@ void launch_one(const LoraArgs& a, hipStream_t st) {
 
 hipError_t launch_lora(const LoraArgs& args, hipStream_t st) {
   LoraArgs a = args;
-  // One launch where a block's A comes faster than a second launch and there is a CU for every block
-  // (a CU alone pulls some 45 bytes a ns).  4096 x 4096, 1 token: rank 8 5.6 us so, 6.7 in two launches; rank 16
-  // 7.0 and 7.1 (the calling thread saves a launch); rank 32 10.9 and 8.1.  1024 x 1024, rank 32, 32
-  // tokens: 5.5 and 9.1.  4096 x 14336, rank 8: 8 tokens 5.8 and 7.8, 16 tokens (448 blocks) 10.9 and 8.5.
+  // One launch where a block's A comes faster than a second launch and there is a CU for every
+  // block.  4096 x 4096, rank 16: 1 token 4.8 us so, 7.2 in two launches, 16 tokens 6.1 and 8.5.
+  // 14336 x 4096, rank 16, 32 tokens (256 blocks): 12.3 and 12.6, 64 tokens 20.2 and 15.6.  4096 x
+  // 4096, rank 32, whose sums take twice the registers: 8 tokens 8.7 and 8.9, 64 tokens 17.2 and
+  // 11.5; 8192 x 8192, 1 token 9.3 and 8.9.
   const int64_t blocks = (int64_t)a.T * ((a.N + 64 * kWaves - 1) / (64 * kWaves));
-  if (a.K <= kOneCols && (int64_t)a.R * a.K <= 1 << 16 && a.R <= 32 && blocks <= 256) {
+  if (a.R <= 32 && blocks <= 256 && (int64_t)a.R * a.K <= (a.R <= 16 ? 1 << 18 : 1 << 17)) {
     if (a.R <= 8)
       launch_one<1>(a, st);
     else if (a.R <= 16)

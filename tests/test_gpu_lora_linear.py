@@ -113,12 +113,13 @@ def test_many_tokens(R, out):
         check(x, a, b, None, scale, of, base, out, in_place=True)
 
 
-@pytest.mark.parametrize("R", [8, 16, 64])
-def test_exact_sums_keep_every_bit(R):
+@pytest.mark.parametrize("T", [19, 270])      # in one launch (ranks up to 32) and in two
+@pytest.mark.parametrize("R", [8, 16, 32, 64])
+def test_exact_sums_keep_every_bit(R, T):
     """Whole numbers whose sums stay below 2^24: fp32 outputs are exact, so nothing of a x is lost on
     its way through the second product."""
     rng = np.random.default_rng(R)
-    T, K, N, n = 19, 640, 130, 4
+    K, N, n = 640, 130, 4
     i = lambda lo, hi, *s: torch.from_numpy(rng.integers(lo, hi + 1, s).astype(np.float32))  # noqa: E731
     x, a, b = i(-9, 9, T, K), i(-9, 9, n, R, K), i(-3, 3, n, N, R)
     of = torch.from_numpy(rng.integers(-1, n, T).astype(np.int32))
@@ -236,11 +237,13 @@ def test_captured_beside_eager_calls_with_a_workspace_each():
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("R", [8, 16, 24, 32])
 def test_one_launch_or_two(R, out):
-    """Small adapters at both sides of the limits of tokens times outputs, columns and both: one kernel
-    for up to 256 blocks of 512 outputs and 65536 elements of a, two beyond."""
+    """Small adapters at both sides of the limits of tokens times outputs and of ranks times columns: one
+    kernel for up to 256 blocks of 512 outputs, and up to 2^18 elements of a (2^17 past rank 16)."""
     rng = np.random.default_rng(R)
     for T, K, N, n in [(256, 72, 40, 7), (257, 72, 40, 7), (300, 1000, 65, 40), (1, 2048, 1500, 3), (2, 2056, 515, 2),
-                       (1, 4096, 33, 2), (3, 4104, 100, 2), (19, 6000, 130, 30), (40, 264, 5000, 9)]:
+                       (1, 4096, 33, 2), (3, 4104, 100, 2), (19, 6000, 130, 30), (40, 264, 5000, 9),
+                       (2, 16384 // R * 8, 70, 2), (2, 16384 // R * 8 + 8, 70, 2), (2, 32768 // R * 8, 70, 2),
+                       (2, 32768 // R * 8 + 8, 70, 2)]:
         print(R, out, T, K, N, n, flush=True)
         x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, out, True, pad=8)
         check(x, a, b, rank, scale, of, base, out, ys=N + 1)
