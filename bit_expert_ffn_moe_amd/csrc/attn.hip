@@ -41,8 +41,8 @@
 // are wanted, so that a wait for one leaves the later ones on their way.  Bound by vector
 // instructions (widening, softmax) and those waits, not by bytes: 8 sequences of 8 kv heads
 // and 8 query heads each over up to 65536 keys of 128 columns, 241 MB, in 59 us (4.1 TB/s;
-// issue 54% busy) and 5 for the join; 32 sequences, 4 query heads each, behind 8192 shared
-// keys, up to 2048 of their own, 43 MB, in 21.5 us and 4.  In the first more or fewer parts took 69 to 114 us, a third tile in flight 70 to 102 (the
+// issue 46% busy) and 5 for the join; 32 sequences, 4 query heads each, behind 8192 shared
+// keys, up to 2048 of their own, 43 MB, in 21.5 us (59%) and 4.  In the first more or fewer parts took 69 to 114 us, a third tile in flight 70 to 102 (the
 // loop's code then no longer fits the instruction cache beside the rest), one wave more a SIMD
 // 164 (registers spilled).
 #include <type_traits>

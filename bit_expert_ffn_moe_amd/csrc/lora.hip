@@ -16,9 +16,9 @@
 // rank leaves room: a rank of 8 takes one instruction, 16 two, 32 three.
 //
 // 4096 tokens of 6 adapters in runs, 4096 x 4096, rank 32, 104 MB and 2.1 GFLOP (HBM alone: 20
-// us): 38.8 us, of which h takes 14.2 (x read once, 35 MB; every block reads its adapters' A
+// us): 39.0 us, of which h takes 14.5 (x read once, 35 MB; every block reads its adapters' A
 // from L2, as many bytes as x), its operands 4.7 and y 20.0 (70 MB; every block of 64 x 64
-// outputs reads its part of B and its tokens' operands from L2; the vector unit is busy 57%
+// outputs reads its part of B and its tokens' operands from L2; the vector unit is busy 55%
 // with that and base + d).  Outputs of 128 or 256 columns a block halve or quarter the
 // operands' reads but leave fewer waves a SIMD: 46 and 57 us.  32 tokens of 24 adapters, ranks
 // up to 64, 4096 x 6144, are a read of their weights (18.7 MB: 3.3 us): h 6.0, y 8.6, each a
