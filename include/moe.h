@@ -491,9 +491,9 @@ size_t attn_workspace_bytes(const kv_cache* cache, int32_t n_seqs, int32_t q_len
  * cache holds at keys that a row does not see (NaN included) does not enter it.  A
  * page number outside the cache hides its keys and sets MOE_STATUS_BAD_PAGE.
  * Scores and sums are fp32.  K and V of an E2M1 cache become bf16 exactly.  For the
- * product with V a key's weight is rounded to bf16; in an E4M3 cache the weight times the key's V scale to fp16, by 2^-11 of
- * itself or by 2^-29 of the row's largest if that is more (V scales up to 2^80
- * apart).
+ * product with V a key's weight is rounded to bf16; in an E4M3 cache the weight times
+ * the key's V scale to fp16, by 2^-11 of itself or by 2^-29 of the row's largest if
+ * that is more (V scales up to 2^80 apart).
  * Sums are formed of weights up to 8 and divided at the end: |v| times 8 times the
  * keys has to stay within fp32's range.
  * n_seqs * q_len <= 262144, n_q_heads <= 1024, n_seqs * q_len * n_q_heads < 2^24
