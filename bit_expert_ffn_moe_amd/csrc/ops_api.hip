@@ -207,6 +207,14 @@ void lora_split(int T, int K, bool* many, int* part_cols, int* parts) {
   *part_cols = each * 1024, *parts = ceil_div(pieces, each);
 }
 
+// What a call of T tokens needs.
+size_t lora_bytes(const lora_weights* w, int T) {
+  bool many;
+  int cols, parts;
+  lora_split(T, w->n_in, &many, &cols, &parts);
+  return up256((size_t)parts * T * w->max_rank * 4) + (many ? up256((size_t)T * 3 * w->max_rank * 2) : 0);
+}
+
 }  // namespace
 
 extern "C" {
@@ -242,10 +250,16 @@ int w4_linear(const w4_weights* w, const uint16_t* x, int64_t x_stride, int32_t 
 
 size_t lora_workspace_bytes(const lora_weights* w, int32_t T) {
   if (check_lora(w) || T < 1 || T > kMaxT) return 0;
-  bool many;
-  int cols, parts;
-  lora_split(T, w->n_in, &many, &cols, &parts);
-  return up256((size_t)parts * T * w->max_rank * 4) + (many ? up256((size_t)T * 3 * w->max_rank * 2) : 0);
+  // Parts get fewer as tokens get more, so some smaller call may need more: the last before the
+  // tokens count as many, or the last of a number of tiles of 32 (512 tiles have one part).
+  size_t n = lora_bytes(w, T);
+  const auto also = [&](int t) {
+    const size_t b = t < T ? lora_bytes(w, t) : 0;
+    n = b > n ? b : n;
+  };
+  also(kLoraMany - 1);
+  for (int t = kLoraMany; t <= 512 * 32; t += 32) also(t);
+  return n;
 }
 
 int lora_linear(const lora_weights* w, const uint16_t* x, int64_t x_stride, int32_t T,
@@ -267,7 +281,7 @@ int lora_linear(const lora_weights* w, const uint16_t* x, int64_t x_stride, int3
   if (T == 0) return MOE_OK;
   if (!ws) return MOE_EINVAL;
   if (!aligned(ws, 256)) return MOE_EALIGN;
-  if (ws_bytes < lora_workspace_bytes(w, T)) return MOE_EWORKSPACE;
+  if (ws_bytes < lora_bytes(w, T)) return MOE_EWORKSPACE;
   rc = check_device();
   if (rc) return rc;
   LoraArgs a;

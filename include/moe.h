@@ -369,7 +369,7 @@ typedef struct lora_weights {
   const float* scale;
 } lora_weights;
 
-/* Workspace bytes of lora_linear for T tokens (0 on invalid arguments). */
+/* Workspace bytes of lora_linear for up to T tokens (0 on invalid arguments). */
 size_t lora_workspace_bytes(const lora_weights* w, int32_t T);
 
 /* y[t] = base[t] + scale_i b_i (a_i x[t]) with i = adapter_of[t]: the adapters of many

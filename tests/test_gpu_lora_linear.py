@@ -270,3 +270,25 @@ def test_two_launches_and_what_is_not_the_tokens():
     same[0] = same[6] = same[8] = same[263] = False
     assert torch.equal(y[same], want[same]) and torch.equal(y[[8, 263]], base[[8, 263], :N])
     assert bool(y[0].isnan().all()) and not bool(y[6].isfinite().any())
+
+
+def test_the_workspace_of_a_large_batch_serves_smaller_ones():
+    """One allocation for up to 2400 tokens, calls of fewer with the bytes that it has: several of them have
+    more parts of x's columns than 2400 have.  Bytes behind it stay as they were."""
+    rng = np.random.default_rng(14)
+    K, N, n, R = 8192, 40, 3, 32
+    w0 = moe.make_lora(n, R, K, N, 256, 256)
+    nb = moe.lora_workspace_bytes(w0, 2400)
+    ws = torch.full((nb + 4096,), 0xAB, dtype=torch.uint8, device=DEV)
+    x, a, b, rank, scale, of, base = make(rng, 2400, K, N, n, R, "f32")
+    w = moe.make_lora(n, R, K, N, a.to(DEV), b.to(DEV), None, scale.to(DEV))
+    e, mag = expect(x, a, b, None, scale, of, base, K)
+    tol = (K + R + 32) * 2.0 ** -23 * mag + 2.0 ** -23 * e.abs()       # as in check()
+    xd, od, based = x.to(DEV), of.to(DEV), base.to(DEV)
+    for T in (1, 33, 1000, 1023, 1024, 1500, 2336, 2337, 2400):
+        print(T, flush=True)
+        y = torch.full((T, N), 5.0, device=DEV)
+        moe.lora_linear(w, xd, K, T, od, based, N, y, N, moe.MOE_DT_F32, None, ws, nb)
+        torch.cuda.synchronize()
+        assert bool(((y.cpu().double() - e[:T]).abs() <= tol[:T]).all())
+        assert bool((ws[nb:] == 0xAB).all())

@@ -85,6 +85,18 @@ def test_lora_null_descriptor_and_workspace():
     assert moe._lib.lora_workspace_bytes(adapters(), (1 << 18) + 1) == 0
 
 
+@pytest.mark.parametrize("K", [128, 4096, 8192, 16384, 20000, 1 << 20])
+@pytest.mark.parametrize("R", [8, 32, 128])
+def test_lora_workspace_of_a_batch_holds_every_smaller_one(R, K):
+    """Parts of x's columns get fewer as tokens get more; the bytes never do."""
+    w = adapters(R=R, K=K)
+    before = 0
+    for T in [*range(1, 1020, 7), *range(1020, 17000), 1 << 17, 1 << 18]:
+        n = moe._lib.lora_workspace_bytes(w, T)
+        assert n >= before, (T, n, before)
+        before = n
+
+
 FULL = dict(history=P, history_stride=50, max_history=50, n_seqs=3, seq_of=P, n_tokens=P, n_prompt=P,
             repetition=P, presence=P, frequency=P, bias_ids=P, bias=P, n_bias=4, mask=P, mask_stride=4,
             n_masks=2, mask_of=P)
