@@ -292,3 +292,78 @@ def test_the_workspace_of_a_large_batch_serves_smaller_ones():
         torch.cuda.synchronize()
         assert bool(((y.cpu().double() - e[:T]).abs() <= tol[:T]).all())
         assert bool((ws[nb:] == 0xAB).all())
+
+
+def cut3(h):
+    """h (float32) as the kernels cut it: three bf16, 8 bits each, cut off."""
+    p = [np.zeros_like(h)] * 3
+    for k in range(3):
+        p[k] = (h.view(np.uint32) & 0xffff0000).view(np.float32)
+        h = h - p[k]
+    return p
+
+
+@pytest.mark.parametrize("T", [19, 270, 1100])      # one launch (ranks up to 32), two, three
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 128])
+def test_every_part_of_h_counts(R, T):
+    """Whole numbers whose sums stay below 2^24, with a x of up to 20 bits: fp32 outputs are exact, and no
+    fewer than three bf16 parts of a x hold it (shown here: without the last one y is another)."""
+    rng = np.random.default_rng(R)
+    K, N, n = 640, 70, 4
+    i = lambda lo, hi, *s: torch.from_numpy(rng.integers(lo, hi + 1, s).astype(np.float32))  # noqa: E731
+    x, a = i(-127, 127, T, K), i(-127, 127, n, R, K)
+    b = torch.zeros((n, N, R))                       # four ranks an output, every rank in one of them
+    for k in range(N):
+        b[:, k, [(4 * k + j) % R for j in range(4)]] = 2 * i(0, 1, n, 4) - 1
+    of = torch.from_numpy((np.arange(T) % (n + 1) - 1).astype(np.int32))
+    base = i(-1000, 1000, T, N)
+    scale = torch.tensor([1.0, 2.0, 0.5, 4.0])
+    e, _ = expect(x, a, b, None, scale, of, base, K)
+    assert float((x.abs() @ a.abs().flatten(0, 1).T).max()) < 2 ** 24
+    for ad in range(n):
+        t = of == ad
+        h = ((x[t].double() @ a[ad].double().T) * float(scale[ad])).numpy()
+        bd = b[ad].double().numpy().T
+        assert (np.abs(h) @ np.abs(bd)).max() + 1000 < 2 ** 23      # (sums of halves too are exact)
+        p = cut3(h.astype(np.float32))
+        assert np.array_equal(p[0].astype(np.float64) + p[1] + p[2], h)
+        less = base[t].double().numpy() + (p[0].astype(np.float64) + p[1]) @ bd
+        assert (p[2] != 0).mean() > 0.1 and (less != e[t].numpy()).any(0).mean() > 0.5
+        assert T < 100 or (p[2] != 0).any(0).all() and (less != e[t].numpy()).any(0).all()
+    y, st = run(x.to(torch.bfloat16), a.to(torch.bfloat16), b.to(torch.bfloat16), None, scale, of, base, "f32")
+    assert st == 0 and torch.equal(y.double(), e)
+
+
+@pytest.mark.parametrize("R", [8, 16, 32, 64, 128])
+def test_many_tokens_and_what_is_not_the_tokens(R):
+    """NaN, infinities and bad numbers of other adapters and tokens from 1024 tokens on."""
+    rng = np.random.default_rng(13)
+    T, K, N, n = 1100, 136, 90, 5
+    x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, "f32", pad=8)
+    rank = torch.tensor([R, 7, 0, R // 2 + 1, R - 7], dtype=torch.int32)
+    of = torch.from_numpy(np.tile(np.array([0, 1, 2, 3, -1], np.int32), T // 5))
+    want = check(x, a, b, rank, scale, of, base, "f32")
+    for i in range(n):
+        r = int(rank[i])
+        a[i, r:], b[i, :, r:] = float("nan"), float("inf")
+    a[4], b[4], x[:, K:], scale[4] = float("nan"), float("nan"), float("nan"), float("nan")
+    x[0], x[6, 3], x[4] = float("nan"), float("inf"), float("nan")
+    of[8], of[1093] = n, 2 ** 31 - 1
+    y, st = run(x, a, b, rank, scale, of, base, "f32")
+    assert st == moe.MOE_STATUS_BAD_INDEX
+    same = torch.ones(T, dtype=torch.bool)
+    same[0] = same[6] = same[8] = same[1093] = False
+    assert torch.equal(y[same], want[same]) and torch.equal(y[[8, 1093]], base[[8, 1093], :N])
+    assert bool(y[0].isnan().all()) and not bool(y[6].isfinite().any())
+
+
+@pytest.mark.parametrize("T,K,N,n,R", [(2048, 14336, 40, 4, 24), (4096, 9000, 70, 3, 64), (1056, 20000, 33, 9, 8),
+                                       (8192, 4096, 64, 2, 16)])
+def test_many_tokens_in_several_passes_a_part(T, K, N, n, R):
+    """So many tokens and columns that a part of x's columns is 2048 or more: a block takes it in passes, the
+    last of them cut short."""
+    rng = np.random.default_rng(T)
+    x, a, b, rank, scale, of, base = make(rng, T, K, N, n, R, "bf16", True, pad=8)
+    check(x, a, b, rank, scale, of, base, "bf16")
+    of = torch.from_numpy((np.arange(T) * n // T).astype(np.int32))      # runs of one adapter
+    check(x, a, b, None, scale, of, base, "bf16", in_place=True)
