@@ -1288,7 +1288,7 @@ void launch_few(const AttnArgs& a, int np, int no, hipStream_t st) {
       attn_part_kernel<D, KV, 2, 1><<<np + no, 256, 0, st>>>(a, np);
       return;
     }
-    if (p2 || s2) {  // (where both are there, the prefix's rows are the more)
+    if (p2 || s2) {  // (where both are there, the prefix's blocks are no smaller: attn_plan)
       attn_part_kernel<D, KV, 2, 2><<<np + no, 256, 0, st>>>(a, np);
       return;
     }

@@ -118,6 +118,11 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   split_rows(c, a->n_tok * a->G, prefix_len, (int64_t)n_seqs * own_keys, &a->prefix_kind,
              &a->prefix_blocks);
   split_rows(c, q_len * a->G, own_keys, 0, &a->own_kind, &a->own_blocks);
+  // Both sorts run in one launch, whose registers leave two waves a SIMD as soon as one of them
+  // takes 32 rows: the prefix's blocks then do too (one sequence of 65 to 128 rows, many E2M1
+  // keys of its own).
+  if (a->own_kind == 2 && a->prefix_kind == 1)
+    a->prefix_kind = 2, a->prefix_blocks = ceil_div(a->n_tok * a->G, 32);
   const int base_p = a->Hkv * a->prefix_blocks;
   // blocks wanted: a prefix one per CU, all together four per CU (half of each at
   // 256 columns, whose blocks take twice the registers)

@@ -402,3 +402,36 @@ def test_graph_replays_of_append_and_attention():
         for name in ("k", "v", "ks", "vs"):
             assert torch.equal(sides[0]["d"][name], sides[1]["d"][name]), (i, name)
         pos.add_(1)
+
+
+# one kv head's rows and keys at both sides of what chooses blocks of 16 or 32 rows or key tiles in LDS
+LIMITS = [
+    (24, 1, 4, 1, 64, 32, 8191, [1 + i % 5 for i in range(24)]),      # 96 rows: shared keys few,
+    (24, 1, 4, 1, 64, 32, 8192, [1 + i % 5 for i in range(24)]),      # or many
+    (24, 1, 4, 1, 128, 32, 8191, [1 + i % 5 for i in range(24)]),
+    (24, 1, 4, 1, 128, 32, 8192, [1 + i % 5 for i in range(24)]),
+    (24, 1, 4, 1, 128, 32, 8192, [1365] + [9] * 23),                  # 24 x 1365 < 4 x 8192 < 24 x 1366
+    (24, 1, 4, 1, 128, 32, 8192, [1366] + [9] * 23),
+    (40, 2, 4, 1, 64, 64, 16384, [2 + i % 5 for i in range(40)]),     # 320 rows: blocks of 32,
+    (40, 2, 4, 1, 64, 64, 16385, [2 + i % 5 for i in range(40)]),     # or key tiles
+    (33, 2, 4, 1, 128, 64, 16385, [2 + i % 5 for i in range(33)]),
+    (1, 80, 4, 1, 64, 64, 0, [16384]),                                # a sequence's own
+    (1, 80, 4, 1, 64, 64, 0, [16385]),
+    (1, 24, 4, 1, 128, 16, 0, [8191]),
+    (1, 24, 4, 1, 128, 16, 0, [8192]),
+    (1, 16, 8, 1, 128, 64, 2000, [9000]),                             # its own by 32 rows behind few shared
+    (1, 16, 8, 1, 64, 64, 2000, [8191]),
+    (1, 16, 8, 1, 64, 64, 2000, [8192]),
+    (1, 17, 4, 1, 128, 64, 10000, [40010]),                           # behind many, four times as many own
+]
+
+
+@pytest.mark.parametrize("shape", LIMITS)
+def test_both_sides_of_what_chooses_the_blocks(shape):
+    B, Q, Hq, Hkv, D, page, P, own = shape
+    print(shape, flush=True)
+    rng = np.random.default_rng(B * 100 + P)
+    kv, q, pre, table, n = build4(rng, B, Q, Hq, Hkv, D, page, P, own)
+    pos = positions(own, P, Q)
+    o, lse = call(kv, q, pos, pre, P, table, n, D ** -0.5, Q)
+    check(o, lse, q, kv, pos, pre, P, table, D ** -0.5, Q, n)

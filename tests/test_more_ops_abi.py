@@ -166,3 +166,12 @@ def test_a_cache_in_4_bits_has_its_scales():
     assert rc() == OK
     assert rc(ks=None) == EINVAL and rc(vs=None) == EINVAL and rc(dt=5) == EINVAL
     assert rc(ks=P + 8) == EALIGN and rc(D=96) == ENOTSUP and rc(page=8) == ENOTSUP
+
+
+def test_blocks_of_32_rows_of_its_own_keys_are_the_prefixs_too():
+    """One sequence of 16 tokens, 8 query heads a kv head, 128 columns: 128 rows over 2000 shared E2M1 keys and
+    9000 of its own, which blocks of 32 rows take.  The shared keys are cut for 8 heads x 4 such blocks and a
+    block a CU: 8 parts.  Its own have 24 (three blocks a CU are left), each a row of sums and weights."""
+    c = ctypes.byref(moe.make_kv_cache(4, 1000, 16, 8, 128, P, P, P, P))
+    rows = 16 * 64
+    assert moe._lib.attn_workspace_bytes(c, 1, 16, 64, 2000, 11000) == (8 + 24) * rows * (8 + 4 * 128)
