@@ -426,8 +426,8 @@ typedef struct kv_cache {
   int32_t pad_;
   void* k;
   void* v;
-  void* k_scale; /* float (E4M3) or uint8_t (E2M1) */
-  void* v_scale;
+  float* k_scale; /* E2M1: its uint8_t, as this pointer */
+  float* v_scale;
 } kv_cache;
 
 /* How pairs are laid out in a rotated head of rope_dim elements: element i

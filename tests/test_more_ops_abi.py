@@ -2,6 +2,8 @@
 happens on the host before any HIP call (no GPU needed), and empty batches are accepted without a
 device."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -175,3 +177,20 @@ def test_blocks_of_32_rows_of_its_own_keys_are_the_prefixs_too():
     c = ctypes.byref(moe.make_kv_cache(4, 1000, 16, 8, 128, P, P, P, P))
     rows = 16 * 64
     assert moe._lib.attn_workspace_bytes(c, 1, 16, 64, 2000, 11000) == (8 + 24) * rows * (8 + 4 * 128)
+
+
+@pytest.mark.parametrize("cc", [["gcc", "-xc", "-std=c99"], ["g++", "-xc++", "-std=c++11"]])
+def test_programs_written_for_an_e4m3_cache_compile(cc):
+    """The scales of a cache descriptor are floats to read and write, without a cast."""
+    src = b"""#include "moe.h"
+static float row_scale(const kv_cache* c, int64_t row) { float* s = c->k_scale; return s[row] * c->v_scale[row]; }
+float use(float* k, float* v) {
+  kv_cache c = {MOE_DT_FP8_E4M3, 1, 16, 1, 64, 0, k, v, k, v};
+  c.k_scale = k;
+  return row_scale(&c, 0);
+}
+"""
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    r = subprocess.run([*cc, "-Wall", "-Werror", "-pedantic", "-fsyntax-only", "-I", inc, "-"], input=src,
+                       capture_output=True, timeout=60)
+    assert r.returncode == 0, r.stderr.decode()
