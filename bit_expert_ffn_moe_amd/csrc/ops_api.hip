@@ -455,7 +455,10 @@ int attn_shared_prefix(const kv_cache* cache, const uint16_t* q, int64_t q_strid
 
 size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top) {
   if (T < 1 || check_logprobs(T, V, n_top)) return 0;
-  return logprob_layout(T, V, n_top).total;
+  // (rows walked by a block each need next to nothing; fewer, which are not, need the more)
+  const size_t few = logprob_layout(T < kLogprobRows ? T : kLogprobRows - 1, V, n_top).total;
+  const size_t n = logprob_layout(T, V, n_top).total;
+  return n > few ? n : few;
 }
 
 int token_logprobs(const void* z, int32_t z_dtype, int64_t row_stride, int32_t T, int32_t V,

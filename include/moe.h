@@ -554,7 +554,7 @@ int logits_adjust(const logits_rules* rules, const void* z, int32_t z_dtype, int
                   int32_t T, int32_t V, void* out, int32_t out_dtype, int64_t out_stride,
                   uint32_t* status, void* stream);
 
-/* Workspace bytes of token_logprobs (0 on invalid arguments). */
+/* Workspace bytes of token_logprobs for up to T rows (0 on invalid arguments). */
 size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top);
 
 /* Log probabilities under softmax(z[t]) of the given tokens, the entropy of the

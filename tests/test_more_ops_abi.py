@@ -194,3 +194,16 @@ float use(float* k, float* v) {
     r = subprocess.run([*cc, "-Wall", "-Werror", "-pedantic", "-fsyntax-only", "-I", inc, "-"], input=src,
                        capture_output=True, timeout=60)
     assert r.returncode == 0, r.stderr.decode()
+
+
+@pytest.mark.parametrize("V", [1, 1000, 50021, 1 << 24])
+@pytest.mark.parametrize("n", [0, 1, 64])
+def test_logprobs_workspace_of_a_batch_holds_every_smaller_one(V, n):
+    """Many rows need no partial results, some smaller batches do; the bytes never fall."""
+    if n > V:
+        pytest.skip("more than there are")
+    before = 0
+    for T in [*range(1, 700), 1000, 1 << 14, 1 << 18]:
+        b = moe._lib.token_logprobs_workspace_bytes(T, V, n)
+        assert b >= before, (T, b, before)
+        before = b
