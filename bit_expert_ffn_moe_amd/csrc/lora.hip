@@ -609,12 +609,17 @@ void launch_one(const LoraArgs& a, hipStream_t st) {
 hipError_t launch_lora(const LoraArgs& args, hipStream_t st) {
   LoraArgs a = args;
   // One launch where a block's A comes faster than a second launch and there is a CU for every
-  // block.  4096 x 4096, rank 16: 1 token 4.8 us so, 7.2 in two launches, 16 tokens 6.1 and 8.5.
-  // 14336 x 4096, rank 16, 32 tokens (256 blocks): 12.3 and 12.6, 64 tokens 20.2 and 15.6.  4096 x
-  // 4096, rank 32, whose sums take twice the registers: 8 tokens 8.7 and 8.9, 64 tokens 17.2 and
-  // 11.5; 8192 x 8192, 1 token 9.3 and 8.9.
+  // block.  4096 x 4096, rank 16, graph replays: 1 token 4.9 us so, 7.3 in two launches, 16 tokens
+  // 5.1 and 8.8, 32 (256 blocks) 7.9 and 9.0, 64 9.3 and 9.6.  14336 x 4096, rank 16, 32 tokens:
+  // 12.3 and 12.6, 64 tokens 20.2 and 15.6.  Past rank 16, whose sums take twice the registers,
+  // the blocks read 2^24 elements of A at most between them: 4096 x 4096, rank 32: 8 tokens 7.7
+  // and 9.1, 16 (2^24) 9.6 and 9.7, 24 11.9 and 10.2, 64 17.5 and 10.1; rank 24: 16 tokens 8.9 and
+  // 9.2, 24 (1.1 x 2^24) 10.6 and 9.6; 2048 x 2048, rank 32, 64 tokens (2^24) 8.7 and 10.0, 128 14.1
+  // and 10.2; 8192 x 8192, rank 32, 1 token 9.3 and 8.9.
   const int64_t blocks = (int64_t)a.T * ((a.N + 64 * kWaves - 1) / (64 * kWaves));
-  if (a.R <= 32 && blocks <= 256 && (int64_t)a.R * a.K <= (a.R <= 16 ? 1 << 18 : 1 << 17)) {
+  const int64_t of_a = (int64_t)a.R * a.K;
+  if (blocks <= 256 && (a.R <= 16 ? of_a <= 1 << 18
+                                  : a.R <= 32 && of_a <= 1 << 17 && blocks * of_a <= 1 << 24)) {
     if (a.R <= 8)
       launch_one<1>(a, st);
     else if (a.R <= 16)

@@ -367,3 +367,14 @@ def test_many_tokens_in_several_passes_a_part(T, K, N, n, R):
     check(x, a, b, rank, scale, of, base, "bf16")
     of = torch.from_numpy((np.arange(T) * n // T).astype(np.int32))      # runs of one adapter
     check(x, a, b, None, scale, of, base, "bf16", in_place=True)
+
+
+@pytest.mark.parametrize("T,K,N,R", [(16, 4096, 4096, 32), (17, 4096, 4096, 32), (21, 4096, 4096, 24),
+                                     (22, 4096, 4096, 24), (256, 2048, 300, 32), (250, 2096, 300, 32),
+                                     (251, 2096, 300, 32)])
+def test_one_launch_or_two_past_rank_16(T, K, N, R):
+    """Both sides of 2^24 elements of a, read by all blocks of 512 outputs together."""
+    rng = np.random.default_rng(T)
+    x, a, b, rank, scale, of, base = make(rng, T, K, N, 3, R, "bf16", True)
+    check(x, a, b, rank, scale, of, base, "bf16")
+    check(x, a, b, None, None, of, base, "bf16", in_place=True)
