@@ -276,3 +276,17 @@ def test_blocks_of_8192_ids_into_the_other_type(zdt, odt):
     r = rules_of(rng, T, V, 900, 20, True, seqs=3)
     for shift in (0, 1):
         check(r, z, V, odt, pad_out=3, shift=shift)
+
+
+@pytest.mark.parametrize("dt,in_place", [("f32", False), ("bf16", False), ("f32", True), ("bf16", True)])
+def test_rows_past_the_grids_own(dt, in_place):
+    """More rows than a grid has (32768): its blocks take several, each with that row's own rules."""
+    rng = np.random.default_rng(5)
+    T, V = 32768 + 517, 67
+    z = torch.from_numpy((3 * rng.standard_normal((T, V))).astype(np.float32)).to(DT[dt][1])
+    r = rules_of(rng, T, V, L=9, nb=2, mask=True, seqs=700)
+    r["seq_of"][32768:] = rng.permutation(700)[:517]
+    check(r, z, V, dt, in_place=in_place)
+    check({k: v for k, v in r.items() if k.startswith("mask")}, z, V, dt, in_place=in_place)
+    r["bias_ids"][32768, 0], r["seq_of"][33000], r["mask_of"][T - 1] = V, 700, r["mask"].shape[0]
+    check(r, z, V, dt, in_place=in_place)
