@@ -389,44 +389,43 @@ __global__ __launch_bounds__(256) void lora_y_kernel(LoraArgs a) {
   }
 }
 
-// y, many tokens: grid (64 NC outputs, 64 tokens).  A wave takes 16 of the tokens; the
+// y, many tokens: grid (64 outputs, 64 tokens).  A wave takes 16 of the tokens; the
 // adapter's weights of these outputs, which lie together in memory, come through LDS for all
 // of them, their 16-byte pieces permuted by row so that the 16 lanes of a group, four
 // rows apart, meet distinct banks.  What does not wait for the adapter's number (base, h) is
 // loaded first, the next adapter's weights under this one's products.
-template <int MODE, int NB, bool BF16, int NC>
+template <int MODE, int NB, bool BF16>
 __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
   constexpr int PR = 4 * NB;                  // pieces of a row in LDS (R / 8 of them are there)
-  constexpr int NL = NB * NC;                 // pieces a thread loads
-  __shared__ uint4 lw[64 * NC * PR];
+  __shared__ uint4 lw[64 * PR];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int tb = blockIdx.y * 64, t0 = tb + 16 * wv, n0 = blockIdx.x * 64 * NC;
+  const int tb = blockIdx.y * 64, t0 = tb + 16 * wv;
+  const int n0 = blockIdx.x * 64, n = n0 + 4 * c;
+  const bool whole = n0 + 64 <= a.N;
   bool bad;
   const int id = adapter_at(a, tb, lane, bad);  // of the block's token l
-  // four outputs of four tokens a chunk; those past the last token stand in as the last
-  Four<BF16> base[NC][4];
+  // four outputs of four tokens; those past the last token stand in as the last
+  Four<BF16> base[4];
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      memset(&base[j][e], 0, sizeof base[j][e]);
-      if (a.base && n0 + 64 * j + 64 <= a.N)
-        base[j][e] = load4<BF16>(a.base, (size_t)min(t0 + 4 * g + e, a.T - 1) * a.base_stride + n0 + 64 * j + 4 * c);
-    }
+  for (int e = 0; e < 4; ++e) {
+    memset(&base[e], 0, sizeof base[e]);
+    if (a.base && whole)
+      base[e] = load4<BF16>(a.base, (size_t)min(t0 + 4 * g + e, a.T - 1) * a.base_stride + n);
+  }
   Rows<MODE, NB> rows;
   rows.load_ready(a, min(t0 + c, a.T - 1), g);
 
   auto place = [](int row, int piece) { return (row * PR + piece) ^ ((row >> 2) & 15); };
   const int pieces = a.R >> 3;                // of a row in memory
   const int ro = g & (MODE - 1);
-  uint4 wreg[NL];
+  uint4 wreg[NB];
   auto load_w = [&](int i) {
     const uint4* wb = reinterpret_cast<const uint4*>(a.b) + (size_t)i * a.N * pieces;
     const size_t from = (size_t)n0 * pieces, last = (size_t)a.N * pieces - 1;
 #pragma unroll
-    for (int l = 0; l < NL; ++l) {
-      const size_t at = from + min(l * 256 + (int)threadIdx.x, 64 * NC * pieces - 1);
+    for (int l = 0; l < NB; ++l) {
+      const size_t at = from + min(l * 256 + (int)threadIdx.x, 64 * pieces - 1);
       wreg[l] = wb[at < last ? at : last];
     }
   };
@@ -441,36 +440,33 @@ __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
     if (i >= 0) {
       __syncthreads();  // (the adapter before is done with LDS)
 #pragma unroll
-      for (int l = 0; l < NL; ++l) {
+      for (int l = 0; l < NB; ++l) {
         const int j = l * 256 + threadIdx.x;
-        if (j < 64 * NC * pieces) lw[place(j / pieces, j % pieces)] = wreg[l];
+        if (j < 64 * pieces) lw[place(j / pieces, j % pieces)] = wreg[l];
       }
       __syncthreads();
     }
     if (next >= 0) load_w(next);
     const int rank = i >= 0 ? rank_of(a, i) : 0;
-    if (ours)
+    if (ours) {
+      v4f_t d[4];
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int n = n0 + 64 * j + 4 * c;
-        v4f_t d[4];
+      for (int k = 0; k < 4; ++k) d[k] = v4f_t{0.f, 0.f, 0.f, 0.f};
+      rows.multiply(g, rank, [&](int b, int k) {
+        return lw[place(4 * c + k, min(4 * b + ro, pieces - 1))];
+      }, d);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[k] = v4f_t{0.f, 0.f, 0.f, 0.f};
-        rows.multiply(g, rank, [&](int b, int k) {
-          return lw[place(64 * j + 4 * c + k, min(4 * b + ro, pieces - 1))];
-        }, d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (!(ours >> (4 * g + e) & 1u)) continue;
-          const int t = t0 + 4 * g + e;
-          if (n0 + 64 * j + 64 <= a.N) {
-            store4<BF16>(a.y, (size_t)t * a.y_stride + n, base[j][e], d[0][e], d[1][e], d[2][e], d[3][e]);
-          } else {
-            const float v[4] = {d[0][e], d[1][e], d[2][e], d[3][e]};
-            store_some<BF16>(a, t, n, v);
-          }
+      for (int e = 0; e < 4; ++e) {
+        if (!(ours >> (4 * g + e) & 1u)) continue;
+        const int t = t0 + 4 * g + e;
+        if (whole) {
+          store4<BF16>(a.y, (size_t)t * a.y_stride + n, base[e], d[0][e], d[1][e], d[2][e], d[3][e]);
+        } else {
+          const float v[4] = {d[0][e], d[1][e], d[2][e], d[3][e]};
+          store_some<BF16>(a, t, n, v);
         }
       }
+    }
     i = next;
   }
 }
@@ -580,12 +576,11 @@ int clamp_to(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : (in
 template <int MODE, int NB>
 void launch_y(const LoraArgs& a, int slots, hipStream_t st) {
   if (a.many) {
-    constexpr int NC = 1;
-    const dim3 grid((a.N + 64 * NC - 1) / (64 * NC), (a.T + 63) / 64);
+    const dim3 grid((a.N + 63) / 64, (a.T + 63) / 64);
     if (a.y_bf16)
-      lora_y_many_kernel<MODE, NB, true, NC><<<grid, 256, 0, st>>>(a);
+      lora_y_many_kernel<MODE, NB, true><<<grid, 256, 0, st>>>(a);
     else
-      lora_y_many_kernel<MODE, NB, false, NC><<<grid, 256, 0, st>>>(a);
+      lora_y_many_kernel<MODE, NB, false><<<grid, 256, 0, st>>>(a);
   } else {
     const dim3 grid((a.N + 255) / 256, (a.T + 15) / 16, slots);
     if (a.y_bf16)
