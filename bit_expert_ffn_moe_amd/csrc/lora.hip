@@ -401,8 +401,7 @@ __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int tb = blockIdx.y * 64, t0 = tb + 16 * wv;
-  const int n0 = blockIdx.x * 64, n = n0 + 4 * c;
-  const bool whole = n0 + 64 <= a.N;
+  const int n0 = blockIdx.x * 64;
   bool bad;
   const int id = adapter_at(a, tb, lane, bad);  // of the block's token l
   // four outputs of four tokens; those past the last token stand in as the last
@@ -410,8 +409,8 @@ __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     memset(&base[e], 0, sizeof base[e]);
-    if (a.base && whole)
-      base[e] = load4<BF16>(a.base, (size_t)min(t0 + 4 * g + e, a.T - 1) * a.base_stride + n);
+    if (a.base && n0 + 64 <= a.N)
+      base[e] = load4<BF16>(a.base, (size_t)min(t0 + 4 * g + e, a.T - 1) * a.base_stride + n0 + 4 * c);
   }
   Rows<MODE, NB> rows;
   rows.load_ready(a, min(t0 + c, a.T - 1), g);
@@ -449,6 +448,7 @@ __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
     if (next >= 0) load_w(next);
     const int rank = i >= 0 ? rank_of(a, i) : 0;
     if (ours) {
+      const int n = n0 + 4 * c;
       v4f_t d[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) d[k] = v4f_t{0.f, 0.f, 0.f, 0.f};
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
       for (int e = 0; e < 4; ++e) {
         if (!(ours >> (4 * g + e) & 1u)) continue;
         const int t = t0 + 4 * g + e;
-        if (whole) {
+        if (n0 + 64 <= a.N) {
           store4<BF16>(a.y, (size_t)t * a.y_stride + n, base[e], d[0][e], d[1][e], d[2][e], d[3][e]);
         } else {
           const float v[4] = {d[0][e], d[1][e], d[2][e], d[3][e]};
