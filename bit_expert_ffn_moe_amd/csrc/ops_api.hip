@@ -121,19 +121,23 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   // Both sorts run in one launch, whose registers leave two waves a SIMD as soon as one of them
   // takes 32 rows: the prefix's blocks then do too (one sequence of 65 to 128 rows, many E2M1
   // keys of its own).
-  if (a->own_kind == 2 && a->prefix_kind == 1)
-    a->prefix_kind = 2, a->prefix_blocks = ceil_div(a->n_tok * a->G, 32);
-  const int base_p = a->Hkv * a->prefix_blocks;
+  const bool raised = prefix_len > 0 && a->prefix_kind == 1 && a->own_kind == 2;
+  if (raised) a->prefix_kind = 2, a->prefix_blocks = ceil_div(a->n_tok * a->G, 32);
   // blocks wanted: a prefix one per CU, all together four per CU (half of each at
-  // 256 columns, whose blocks take twice the registers)
-  const int want_p = a->D == 256 ? 128 : 256, want = 4 * want_p;
+  // 256 columns, whose blocks take twice the registers).  A short prefix whose blocks were
+  // raised: one per two CUs, counted as one (8 kv heads of 128 columns, 128 rows, 2000 shared
+  // keys, 9000 own: 28.1 us, 29.9 with one per CU; 96 rows, 7000 and 12000: 26.6, 30.4; 128 rows,
+  // 8000 and 41000: 28.5, 32.9; 10000 and 41000: one per CU 34.0, one per two 37.7)
+  const int per_cu = a->D == 256 ? 128 : 256, want = 4 * per_cu;
+  const int want_p = raised && prefix_len < 8192 ? per_cu / 2 : per_cu;
+  const int base_p = a->Hkv * a->prefix_blocks;
   split_keys(prefix_len, a->prefix_kind, base_p,
              a->prefix_kind == kAttnTile ? 256 : want_p, &a->prefix_chunk, &a->n_prefix_parts);
   const int taken = a->prefix_kind != kAttnTile && a->own_kind != kAttnTile
-                        ? base_p * a->n_prefix_parts
+                        ? (raised ? per_cu : base_p * a->n_prefix_parts)
                         : 0;
   split_keys(max_keys > prefix_len ? max_keys - (prefix_len & ~31) : 0, a->own_kind,
-             a->B * a->Hkv * a->own_blocks, want - taken < want_p ? want_p : want - taken,
+             a->B * a->Hkv * a->own_blocks, want - taken < per_cu ? per_cu : want - taken,
              &a->own_chunk, &a->n_own_parts);
   return MOE_OK;
 }

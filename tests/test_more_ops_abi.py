@@ -170,13 +170,15 @@ def test_a_cache_in_4_bits_has_its_scales():
     assert rc(ks=P + 8) == EALIGN and rc(D=96) == ENOTSUP and rc(page=8) == ENOTSUP
 
 
-def test_blocks_of_32_rows_of_its_own_keys_are_the_prefixs_too():
-    """One sequence of 16 tokens, 8 query heads a kv head, 128 columns: 128 rows over 2000 shared E2M1 keys and
-    9000 of its own, which blocks of 32 rows take.  The shared keys are cut for 8 heads x 4 such blocks and a
-    block a CU: 8 parts.  Its own have 24 (three blocks a CU are left), each a row of sums and weights."""
+@pytest.mark.parametrize("shared,own,parts", [(10000, 41000, 8 + 23), (2000, 9000, 4 + 24), (0, 9000, 24)])
+def test_blocks_of_32_rows_of_its_own_keys_are_the_prefixs_too(shared, own, parts):
+    """One sequence of 16 tokens, 8 kv heads of 8 query heads, 128 columns: 128 rows over shared E2M1 keys and many
+    of its own, which blocks of 32 rows take.  The shared keys are cut for 8 heads x 4 such blocks and a
+    block a CU (few of them: a block for two), the own for the three blocks a CU that are left.  Each
+    part leaves a row's maximum, sum and columns."""
     c = ctypes.byref(moe.make_kv_cache(4, 1000, 16, 8, 128, P, P, P, P))
     rows = 16 * 64
-    assert moe._lib.attn_workspace_bytes(c, 1, 16, 64, 2000, 11000) == (8 + 24) * rows * (8 + 4 * 128)
+    assert moe._lib.attn_workspace_bytes(c, 1, 16, 64, shared, shared + own) == parts * rows * (8 + 4 * 128)
 
 
 @pytest.mark.parametrize("cc", [["gcc", "-xc", "-std=c99"], ["g++", "-xc++", "-std=c++11"]])
