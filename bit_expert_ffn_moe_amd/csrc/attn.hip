@@ -42,9 +42,14 @@
 // instructions (widening, softmax) and those waits, not by bytes: 8 sequences of 8 kv heads
 // and 8 query heads each over up to 65536 keys of 128 columns, 241 MB, in 59 us (4.1 TB/s;
 // issue 46% busy) and 5 for the join; 32 sequences, 4 query heads each, behind 8192 shared
-// keys, up to 2048 of their own, 43 MB, in 21.5 us (59%) and 4.  In the first more or fewer parts took 69 to 114 us, a third tile in flight 70 to 102 (the
-// loop's code then no longer fits the instruction cache beside the rest), one wave more a SIMD
-// 164 (registers spilled).
+// keys, up to 2048 of their own, 43 MB, in 21.5 us (59%) and 4.  In the first more or fewer
+// parts took 69 to 114 us, a third tile in flight 70 to 102 (the loop's code then no longer fits
+// the instruction cache beside the rest), one wave more a SIMD 164 (registers spilled).  The
+// weights are rounded to bf16, as beside bf16 V, because V's scales reach over bf16's exponents
+// and a weight would need one per 32 columns to be fp16 instead: outputs of these two cases are
+// 0.0019 and 0.0020 off in the 2-norm, with weights of 32 bits 0.0017, which is their own rounding.
+// At 256 columns 32 sequences of 8 kv heads, 4 query heads each, behind 8192 and 2048 keys take
+// 75.7 us and 5.3; 16 registers spill there.
 #include <type_traits>
 
 #include "common.h"
@@ -445,7 +450,8 @@ __device__ __forceinline__ void attn_item(const AttnArgs& a, int h, int t0, int 
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           if constexpr (FP4) {
-            kf[u][s] = fp4x8(raw.kq[u][s], fp4_scale(D == 256 ? raw.ksb[u] >> 8 * (s >> 2) & 0xffu : raw.ksb[u]));
+            const uint32_t b = D == 256 ? raw.ksb[u] >> 8 * (s >> 2) & 0xffu : raw.ksb[u];
+            kf[u][s] = fp4x8(raw.kq[u][s], fp4_scale(b));
           } else if constexpr (FP8) {
             const uint4 k = kr[u][s / 2];
             kf[u][s] = (s & 1) ? fp8x8(k.z, k.w) : fp8x8(k.x, k.y);
@@ -800,7 +806,8 @@ __global__ __launch_bounds__(256, D < 256 && RTP == 1 ? 3 : 2) void attn_part_ke
 // Bound by the vector unit (a score costs an exponential and six more operations, with
 // an FP8 cache's two scales) and the matrix cores in turn: 512 rows of 8 kv heads
 // over 32768 keys, 69 GFLOP, 114 us bf16 with the join, 113 us FP8 without it, the
-// matrix cores busy for 27% of that.  (Forming the scores of the next 32 keys
+// matrix cores busy for 27% of that; 1024 rows of 8 kv heads over 32768 E2M1 keys, 138 GFLOP, 198
+// us without it.  (Forming the scores of the next 32 keys
 // under the exponentials of these takes the registers that hide LDS and loads: 170
 // us bf16.)
 template <int D, int KV, int RT>

@@ -16,12 +16,12 @@
 // rank leaves room: a rank of 8 takes one instruction, 16 two, 32 three.
 //
 // 4096 tokens of 6 adapters in runs, 4096 x 4096, rank 32, 104 MB and 2.1 GFLOP (HBM alone: 20
-// us): 39.0 us, of which h takes 14.5 (x read once, 35 MB; every block reads its adapters' A
-// from L2, as many bytes as x), its operands 4.7 and y 20.0 (70 MB; every block of 64 x 64
-// outputs reads its part of B and its tokens' operands from L2; the vector unit is busy 55%
+// us): 39.9 us, of which h takes 14.9 (x read once, 35 MB; every block reads its adapters' A
+// from L2, as many bytes as x), its operands 4.6 and y 20.2 (70 MB; every block of 64 x 64
+// outputs reads its part of B and its tokens' operands from L2; the vector unit is busy 56%
 // with that and base + d).  Outputs of 128 or 256 columns a block halve or quarter the
 // operands' reads but leave fewer waves a SIMD: 46 and 57 us.  32 tokens of 24 adapters, ranks
-// up to 64, 4096 x 6144, are a read of their weights (18.7 MB: 3.3 us): h 6.0, y 8.6, each a
+// up to 64, 4096 x 6144, are a read of their weights (18.7 MB: 3.3 us): h 6.0, y 8.5, each a
 // launch and three dependent trips to memory (numbers, rank and weights, result).
 #include <string.h>
 
@@ -394,6 +394,11 @@ __global__ __launch_bounds__(256) void lora_y_kernel(LoraArgs a) {
 // of them, their 16-byte pieces permuted by row so that the 16 lanes of a group, four
 // rows apart, meet distinct banks.  What does not wait for the adapter's number (base, h) is
 // loaded first, the next adapter's weights under this one's products.
+//
+// Five waves a SIMD suit one block of ranks (96 registers).  Two and four blocks of ranks, up to 64
+// and 128, need more and keep 84 and 352 bytes a lane in scratch: 4096 tokens, 4096 x 4096, bf16,
+// rank 32: 20.2 us, 64: 39.8, 128: 142.  Ranks up to 16 read their zeros through 32 bytes of it:
+// rank 8 14.6, rank 16 15.8.
 template <int MODE, int NB, bool BF16>
 __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {
   constexpr int PR = 4 * NB;                  // pieces of a row in LDS (R / 8 of them are there)

@@ -118,7 +118,7 @@ int attn_plan(const kv_cache* c, int n_seqs, int q_len, int n_q_heads, int prefi
   split_rows(c, a->n_tok * a->G, prefix_len, (int64_t)n_seqs * own_keys, &a->prefix_kind,
              &a->prefix_blocks);
   split_rows(c, q_len * a->G, own_keys, 0, &a->own_kind, &a->own_blocks);
-  // Both sorts run in one launch, whose registers leave two waves a SIMD as soon as one of them
+  // Both sorts run in one launch, whose registers leave fewer waves a SIMD as soon as one of them
   // takes 32 rows: the prefix's blocks then do too (one sequence of 65 to 128 rows, many E2M1
   // keys of its own).
   const bool raised = prefix_len > 0 && a->prefix_kind == 1 && a->own_kind == 2;

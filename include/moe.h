@@ -375,8 +375,9 @@ size_t lora_workspace_bytes(const lora_weights* w, int32_t T);
 /* y[t] = base[t] + scale_i b_i (a_i x[t]) with i = adapter_of[t]: the adapters of many
  * requests beside a projection that they share (base: what w4_linear or another
  * product left).  a_i x is kept in fp32, both products accumulate in fp32, y is
- * rounded once.  (a_i x meets b_i in three bf16 parts that add up to it, so an
- * infinite element of b may give NaN.)
+ * rounded once.  An infinite element of b gives its infinity or NaN, by the number
+ * of tokens and the bits of a_i x (which meets b_i in three bf16 parts that add up
+ * to it; a part of 0 gives NaN).
  *   x [T][n_in] bf16, rows x_stride apart (a multiple of 8, >= n_in)
  *   adapter_of [T] int32; negative: none (y = base).  An index >= n_adapters is none
  *     too and sets MOE_STATUS_BAD_INDEX.  Tokens of one adapter need not be
