@@ -396,8 +396,8 @@ __global__ __launch_bounds__(256) void lora_y_kernel(LoraArgs a) {
 // loaded first, the next adapter's weights under this one's products.
 //
 // Five waves a SIMD suit one block of ranks (96 registers).  Two and four blocks of ranks, up to 64
-// and 128, need more and keep 84 and 352 bytes a lane in scratch: 4096 tokens, 4096 x 4096, bf16,
-// rank 32: 20.2 us, 64: 39.8, 128: 142.  Ranks up to 16 read their zeros through 32 bytes of it:
+// and 128, need more and keep 84 and 368 or 400 bytes a lane in scratch: 4096 tokens, 4096 x 4096,
+// bf16, rank 32: 20.2 us, 64: 39.8, 128: 142.  Ranks up to 16 read their zeros through 32 bytes of it:
 // rank 8 14.6, rank 16 15.8.
 template <int MODE, int NB, bool BF16>
 __global__ __launch_bounds__(256, 5) void lora_y_many_kernel(LoraArgs a) {

@@ -185,6 +185,7 @@ class Session:
         self.text = torch.zeros((B, self.P + max_new), **i32)       # the prompt, then what is generated
         self.text[:, :self.P] = prompt.to(DEV)
         self.n_tokens, self.n_prompt = (torch.full((B,), self.P, **i32) for _ in range(2))
+        self.last = torch.full((B,), self.text.shape[1] - 1, device=DEV)
         self.bias_ids = (ids[:, None] * 97 + torch.arange(4, device=DEV) * 13).remainder(c.vocab).int()
         self.bias = torch.linspace(-2, 2, 4, device=DEV).expand(B, 4).contiguous()
         self.mask = torch.full((1, -(-c.vocab // 32)), 0x55555555, **i32)   # the even tokens
@@ -256,8 +257,9 @@ class Session:
                         moe.MOE_DT_BF16)
         self._norm(2, self.ffn, self.stream, B, None, self.xn)
         moe.w4_linear(b.vocab, self.xn, c.hidden, B, self.logits, c.vocab, moe.MOE_DT_F32)
-        # the token that this step took is part of the text now
-        self.text.scatter_(1, self.n_tokens[:, None].long(), self.token[:, None])
+        # the token that this step took is part of the text now (past max_new in the last place: the
+        # status says so)
+        self.text.scatter_(1, torch.minimum(self.n_tokens, self.last)[:, None], self.token[:, None])
         self.n_tokens.add_(1)
         moe.logits_adjust(self.rules, self.logits, moe.MOE_DT_F32, c.vocab, B, c.vocab, self.ruled,
                           moe.MOE_DT_F32, c.vocab, self.status)

@@ -157,3 +157,18 @@ def test_a_captured_step_replays_as_eager_steps(fp4):
                   "xq", "xs", "ffn", "k", "v"):
             assert torch.equal(getattr(eager, n), getattr(cap, n)), (i, n)
     assert int(cap.status.item()) == 0
+
+
+def test_steps_past_the_last_new_token_are_refused_by_the_status():
+    """The text is full after `new` tokens: a further step stays inside it and says so."""
+    s = session(True, B=3, P=20, new=2)
+    for _ in range(2):
+        s.step()
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0
+    text = s.text.clone()
+    for _ in range(2):
+        s.step()
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == moe.MOE_STATUS_BAD_PAGE | moe.MOE_STATUS_BAD_INDEX
+    assert torch.equal(s.text[:, :-1], text[:, :-1])
